@@ -29,36 +29,18 @@
 #include <string.h>
 
 #include <algorithm>
-#include <atomic>
 #include <mutex>
 #include <type_traits>
 #include <vector>
 
-#include "fs_plan_impl.h"
+#include "fs_device.h"
 #include "../../include/fs_bench.h"
 
-using fsi::BufInfo;
-using fsi::Segment;
-using fsi::Tile;
+using namespace fsi;
 
 namespace {
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
-constexpr int kThreads = fsi::kThreads;
-
-__host__ __device__ __forceinline__ int64_t imax(int64_t a, int64_t b) { return a > b ? a : b; }
-__host__ __device__ __forceinline__ int64_t imin(int64_t a, int64_t b) { return a < b ? a : b; }
-
 // ---------------------------------------------------------------- memory --
-
-__device__ __forceinline__ u32x4 ld16(const char *p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
-}
-__device__ __forceinline__ void st16(char *p, u32x4 v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
-}
 
 // Bytes [sh, sh+16) of the 32-byte window lo:hi (sh in 0..15): a two-level
 // word select (by 2 words, then by 1) followed by a byte align.  Written with
@@ -76,37 +58,6 @@ __device__ __forceinline__ u32x4 funnel16(u32x4 lo, u32x4 hi, uint32_t sh) {
     o.z = __builtin_amdgcn_alignbyte(a3, a2, r);
     o.w = __builtin_amdgcn_alignbyte(a4, a3, r);
     return o;
-}
-
-// Select mask of the elements [e_lo, e_hi) of a 16-byte block (W-byte elements).
-template <int W>
-__device__ __forceinline__ u32x4 elem_mask(int e_lo, int e_hi) {
-    uint32_t m[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (W == 4) {
-            m[i] = (i >= e_lo && i < e_hi) ? 0xFFFFFFFFu : 0u;
-        } else {
-            uint32_t lo = (2 * i >= e_lo && 2 * i < e_hi) ? 0x0000FFFFu : 0u;
-            uint32_t hi = (2 * i + 1 >= e_lo && 2 * i + 1 < e_hi) ? 0xFFFF0000u : 0u;
-            m[i] = lo | hi;
-        }
-    }
-    return u32x4{m[0], m[1], m[2], m[3]};
-}
-
-template <int W>
-__device__ __forceinline__ void store_elems(char *dst, u32x4 v, int e_lo, int e_hi) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 16 / W; ++e) {
-        if (e >= e_lo && e < e_hi) {
-            if (W == 4)
-                *reinterpret_cast<uint32_t *>(dst + 4 * e) = w[e];
-            else
-                *reinterpret_cast<uint16_t *>(dst + 2 * e) = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        }
-    }
 }
 
 // --------------------------------------------------------- pack / unpack --
@@ -375,12 +326,6 @@ __global__ __launch_bounds__(kThreads) void unpack_kernel(const Segment *__restr
 // six workgroups per CU this measured 3% faster on the 7B groups than whole
 // blocks per lane (two 16-byte loads 32 bytes apart, one 16-byte store)
 // uncapped, which had been 4% faster than one block at a time.
-
-__device__ __forceinline__ uint16_t bf16_rne_bits(uint32_t u) {
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);   // quiet NaN
-    u += 0x7FFFu + ((u >> 16) & 1u);
-    return (uint16_t)(u >> 16);
-}
 
 __device__ __forceinline__ u32x4 cvt8_bf16(u32x4 a, u32x4 b) {
     return u32x4{(uint32_t)bf16_rne_bits(a.x) | ((uint32_t)bf16_rne_bits(a.y) << 16),
@@ -1208,7 +1153,6 @@ constexpr int kAdamWgsPerCu = 12;      // adamw_kernel (one wave per workgroup)
 constexpr int kUnpackWgsPerCu = 6;     // unpack_kernel (registers allow 7-8)
 constexpr int kReshardWgsPerCu = 6;    // scatter_kernel<W, UnpackSrc> (registers allow 8)
 constexpr int kCastWgsPerCu = 6;       // pack_cast_kernel (registers allow 8)
-constexpr int64_t kCapMinRounds = 16;
 
 // Long calls run as consecutive launches over sub-ranges of at most kSpan
 // elements (kRsSpan for the bf16 reduce dtype, kAdamSpan for AdamW), one
@@ -1226,45 +1170,6 @@ constexpr int64_t kCapMinRounds = 16;
 constexpr int64_t kSpan = 32ll << 20;
 constexpr int64_t kRsSpan = 16ll << 20;
 constexpr int64_t kAdamSpan = 64ll << 20;
-
-struct CuLimits {
-    int lds_per_cu = 0, lds_per_wg = 0, cus = 0;   // 0: unknown, no cap
-};
-
-CuLimits cu_limits() {
-    constexpr int kMaxDev = 64;
-    static std::atomic<int> lds_cu[kMaxDev], lds_wg[kMaxDev], ncu[kMaxDev];   // 0: not read yet, -1: failed
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDev) return {};
-    if (lds_cu[dev].load(std::memory_order_acquire) == 0) {
-        int a = 0, b = 0, c = 0;
-        const bool ok = hipDeviceGetAttribute(&a, hipDeviceAttributeMaxSharedMemoryPerMultiprocessor, dev) ==
-                            hipSuccess &&
-                        hipDeviceGetAttribute(&b, hipDeviceAttributeMaxSharedMemoryPerBlock, dev) == hipSuccess &&
-                        hipDeviceGetAttribute(&c, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess &&
-                        a > 0 && b > 0 && c > 0;
-        lds_wg[dev].store(ok ? b : -1, std::memory_order_relaxed);
-        ncu[dev].store(ok ? c : -1, std::memory_order_relaxed);
-        lds_cu[dev].store(ok ? a : -1, std::memory_order_release);
-    }
-    CuLimits L;
-    if (lds_cu[dev].load(std::memory_order_acquire) < 0) return L;
-    L.lds_per_cu = lds_cu[dev].load(std::memory_order_relaxed);
-    L.lds_per_wg = lds_wg[dev].load(std::memory_order_relaxed);
-    L.cus = ncu[dev].load(std::memory_order_relaxed);
-    return L;
-}
-
-// Dynamic LDS bytes for a grid of `grid` workgroups capped at k per CU, for a
-// kernel that already uses `static_bytes` of LDS (0: no cap).
-uint32_t lds_cap(int k, int64_t grid, int64_t static_bytes = 0) {
-    const CuLimits L = cu_limits();
-    if (L.lds_per_cu <= 0 || k < 1) return 0;
-    if (grid < kCapMinRounds * k * (int64_t)L.cus) return 0;
-    const int64_t per_wg = L.lds_per_cu / (k + 1) + 1;   // k of these fit in a CU, k + 1 do not
-    if (per_wg > L.lds_per_wg || per_wg * k > L.lds_per_cu || per_wg <= static_bytes) return 0;
-    return (uint32_t)(per_wg - static_bytes);
-}
 
 int check_hparams(const char *what, const fs_adamw_hparams_t *hp) {
     if (!hp) return fsi::fail(FS_E_INVAL, "%s: hp is NULL", what);
@@ -1284,8 +1189,6 @@ int check_device(const char *what, int dev_id) {
     return FS_OK;
 }
 
-bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
 // A plan's workspace holds the tables its kernels read, so it must be
 // device memory of the current device; *dev receives that device.
 int check_workspace(const char *what, const void *ws, int *dev) {
@@ -1298,12 +1201,6 @@ int check_workspace(const char *what, const void *ws, int *dev) {
     }
     if (a.type != hipMemoryTypeDevice || a.device != *dev)
         return fsi::fail(FS_E_INVAL, "%s: workspace must be device memory of the current device (%d)", what, *dev);
-    return FS_OK;
-}
-
-int check_launch(const char *what) {
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fsi::fail(FS_E_HIP, "%s: kernel launch failed: %s", what, hipGetErrorString(e));
     return FS_OK;
 }
 
@@ -1363,11 +1260,6 @@ void launch_reduce_pass(int64_t n, int64_t off, int64_t len, hipStream_t stream,
 // lane per 8 elements.
 bool grid_fits(int64_t n) {
     return (n + kAdamRow - 1) / kAdamRow <= INT32_MAX && ((n >> 3) + kThreads - 1) / kThreads <= INT32_MAX;
-}
-
-bool ranges_overlap(const void *a, int64_t abytes, const void *b, int64_t bbytes) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return abytes > 0 && bbytes > 0 && x < y + (uintptr_t)bbytes && y < x + (uintptr_t)abytes;
 }
 
 // Index of the first of `cnt` buffers that overlaps an earlier one, or -1.
