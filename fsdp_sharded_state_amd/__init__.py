@@ -11,6 +11,12 @@ functions raises.
     fs_unpack(plan, gathered, outs)       # all-gather copy-out
     fs_reduce_shard(slices, grad32, world=8, grad_acc=4)
     fs_adamw_step(master, m, v, grad32, p16, lr=1e-3, step=1)
+
+With clipping by the global norm (`total` goes through an all-reduce when the
+ranks are processes):
+
+    fs_reduce_shard_norm(slices, grad32, total, world=8, grad_acc=4)
+    fs_adamw_step_clip(master, m, v, grad32, p16, total=total, max_norm=1.0, step=1)
 """
 from __future__ import annotations
 
@@ -31,6 +37,7 @@ _CODES = {0: "FS_OK", -1: "FS_E_INVAL", -2: "FS_E_UNSUPPORTED", -3: "FS_E_DTYPE"
 FS_BF16, FS_FP32 = 0, 1
 NOALLOC_MAX_NUMEL = 16777216   # scratch capacity of fs_reduce_adamw_step_noalloc (fp32 elements)
 FS_FSDP1_FLAT, FS_FSDP2_PER_PARAM = 1, 2
+FS_NORM_L2, FS_NORM_INF = 1, 2
 
 
 class FsError(RuntimeError):
@@ -69,6 +76,11 @@ class AdamWHparams(ctypes.Structure):
                 ("step", ctypes.c_int64)]
 
 
+class Clip(ctypes.Structure):
+    _fields_ = [("total", ctypes.c_void_p), ("max_norm", ctypes.c_float), ("eps", ctypes.c_float),
+                ("norm_type", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -104,6 +116,13 @@ def lib() -> ctypes.CDLL:
     L.fs_load_local.argtypes = [vp, i32, vp, vp, vp]
     L.fs_reduce_adamw_step_noalloc.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, ctypes.POINTER(AdamWHparams), vp]
     L.fs_reduce_adamw_step.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, vp, ctypes.POINTER(AdamWHparams), vp]
+    L.fs_grad_norm.argtypes = [i32, vp, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    L.fs_grad_norm_workspace.argtypes = [i32, vp, vp, ctypes.POINTER(i64)]
+    L.fs_clip_grads.argtypes = [i32, vp, vp, vp, ctypes.POINTER(Clip), vp, vp]
+    L.fs_reduce_shard_norm.argtypes = [i64, i32, i32, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    L.fs_reduce_shard_norm_workspace.argtypes = [i64, ctypes.POINTER(i64)]
+    L.fs_adamw_step_clip.argtypes = [i64, vp, vp, vp, vp, i32, vp, ctypes.POINTER(AdamWHparams), ctypes.POINTER(Clip),
+                                     vp]
     L.fs_copy_bytes.argtypes = [vp, vp, i64, vp]
     L.fs_stream_read.argtypes = [vp, i64, vp, vp]
     L.fs_stream_fill.argtypes = [vp, i64, ctypes.c_uint32, vp]
@@ -113,6 +132,8 @@ def lib() -> ctypes.CDLL:
                  "fs_pack", "fs_unpack", "fs_reduce_shard", "fs_adamw_step", "fs_reduce_adamw_step",
                  "fs_reduce_shard_ex", "fs_pack_cast", "fs_reshard_plan", "fs_reshard_info",
                  "fs_reshard_upload", "fs_reshard", "fs_load_local", "fs_reduce_adamw_step_noalloc",
+                 "fs_grad_norm", "fs_grad_norm_workspace", "fs_clip_grads", "fs_reduce_shard_norm",
+                 "fs_reduce_shard_norm_workspace", "fs_adamw_step_clip",
                  "fs_copy_bytes", "fs_stream_read", "fs_stream_fill"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -536,6 +557,180 @@ def fs_reduce_adamw_step_noalloc(slices: Sequence[torch.Tensor], master: torch.T
     _check(lib().fs_reduce_adamw_step_noalloc(n, int(world), int(grad_acc), arr, ptr(master, "master"),
                                               ptr(exp_avg, "exp_avg"), ptr(exp_avg_sq, "exp_avg_sq"),
                                               ptr(param_bf16, "param_bf16"), ctypes.byref(hp), _stream(stream)))
+
+
+def _norm_code(norm_type) -> int:
+    p = float(norm_type)
+    if p == 2.0:
+        return FS_NORM_L2
+    if p == math.inf:
+        return FS_NORM_INF
+    raise ValueError(f"unsupported norm_type {norm_type!r}: 2 and inf are defined")
+
+
+class GradList:
+    """A list of gradient tensors (or of reduce slices) that is handed to
+    several calls: their addresses, element counts and types, looked up once.
+
+    The tensors' memory is held, not the tensor objects' identity: a gradient
+    that is replaced (`p.grad = other`, `p.data = other`) needs a new list.  A
+    storage that has been resized since is noticed and refused."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor]):
+        n = len(tensors)
+        ptrs, numels, codes, device, storages = [], [], [], None, {}
+        for i, t in enumerate(tensors):
+            ptrs.append(_dev_ptr(t, f"tensor {i}"))
+            numels.append(t.numel())
+            codes.append(_dtype_code(t.dtype))
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {device}")
+            st = t.untyped_storage()
+            storages[st.data_ptr()] = (st, st.data_ptr(), st.nbytes())
+        self.device: Optional[torch.device] = device
+        self.numels, self.codes = numels, codes
+        self._storages = list(storages.values())
+        self._tensors = [t.detach() for t in tensors]   # aliases: they keep the memory
+        self._n = n
+        self._ptrs = (ctypes.c_void_p * max(1, n))(*ptrs)
+        self._numels = (ctypes.c_int64 * max(1, n))(*numels)
+        self._codes = (ctypes.c_int32 * max(1, n))(*codes)
+        need = ctypes.c_int64()
+        _check(lib().fs_grad_norm_workspace(n, self._numels, self._codes, ctypes.byref(need)))
+        self._norm_bytes = need.value
+
+    def __len__(self) -> int:
+        return self._n
+
+    def _live(self) -> "GradList":
+        for st, ptr, nbytes in self._storages:
+            if st.data_ptr() != ptr or st.nbytes() != nbytes:
+                raise ValueError("a tensor of the list no longer has the memory it had when the list was made")
+        return self
+
+
+def fs_grad_list(tensors: Sequence[torch.Tensor]) -> GradList:
+    """A list of bf16 and fp32 gradients on one GPU, for fs_grad_norm,
+    fs_clip_grads and (bf16, one size) fs_reduce_shard_norm."""
+    return GradList(tensors)
+
+
+def _grad_list(tensors) -> GradList:
+    return tensors._live() if isinstance(tensors, GradList) else GradList(tensors)
+
+
+def _scalar_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, device, what: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError(f"{what} must be one {dtype} value")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the gradients on {device}")
+    return _dev_ptr(t, what)
+
+
+def _launch(device: torch.device, stream, fn, *args, scratch: int = -1):
+    """Run a launching call with `device` current, on `stream` (default: that
+    device's current stream).  scratch >= 0: that many workspace bytes and
+    their count go before the stream; they belong to the stream the kernels
+    run on, so the allocator hands them out again in that stream's order."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(device, stream, fn, *args, scratch=scratch)
+    handle = _stream(stream)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if scratch < 0:
+        return _check(fn(*args, handle))
+    if scratch == 0:
+        return _check(fn(*args, None, 0, handle))
+    if stream is None:
+        ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+    else:
+        own = (stream if isinstance(stream, torch.cuda.Stream) else
+               torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
+        with torch.cuda.stream(own):
+            ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+    return _check(fn(*args, ws.data_ptr(), scratch, handle))
+
+
+def fs_grad_norm(grads, total: torch.Tensor, norm: Optional[torch.Tensor] = None, *, norm_type=2.0,
+                 accumulate: bool = False, stream=None):
+    """Total (float64, one value: the sum of squares, or with norm_type inf
+    the largest magnitude) and norm (float32, one value) of a list of bf16 and
+    fp32 gradients: a sequence of tensors or a GradList.  accumulate: joined
+    to the total that stands there."""
+    kind = _norm_code(norm_type)
+    gl = _grad_list(grads)
+    tot = _scalar_ptr(total, torch.float64, gl.device, "total")
+    nrm = _scalar_ptr(norm, torch.float32, total.device, "norm")
+    _launch(total.device, stream, lib().fs_grad_norm, gl._n, gl._ptrs, gl._numels, gl._codes, kind, int(accumulate),
+            tot, nrm, scratch=gl._norm_bytes)
+
+
+def fs_clip_grads(grads, total: torch.Tensor, max_norm: float, norm: Optional[torch.Tensor] = None, *, norm_type=2.0,
+                  norm_eps: float = 1e-6, stream=None):
+    """Scale a list of gradients in place by min(1, max_norm / (norm_of(total)
+    + norm_eps)); norm (float32, one value) receives the norm of the total."""
+    kind = _norm_code(norm_type)
+    gl = _grad_list(grads)
+    clip = Clip(_scalar_ptr(total, torch.float64, gl.device, "total"), max_norm, norm_eps, kind)
+    nrm = _scalar_ptr(norm, torch.float32, total.device, "norm")
+    _launch(total.device, stream, lib().fs_clip_grads, gl._n, gl._ptrs, gl._numels, gl._codes, ctypes.byref(clip), nrm)
+
+
+def fs_reduce_shard_norm(slices, out: torch.Tensor, total: torch.Tensor, norm: Optional[torch.Tensor] = None, *,
+                         world: int, grad_acc: int = 1, reduce_dtype="fp32", norm_type=2.0,
+                         accumulate: bool = False, stream=None):
+    """fs_reduce_shard_ex (slices: a sequence or a GradList), and the total and
+    norm of the averaged gradients, as fs_grad_norm gives them for out."""
+    kind = _norm_code(norm_type)
+    n = out.numel()
+    if out.dtype != torch.float32:
+        raise ValueError("fs_reduce_shard_norm: out must be float32")
+    if len(slices) != world * grad_acc:
+        raise ValueError(f"fs_reduce_shard_norm: need world*grad_acc = {world * grad_acc} slices")
+    gl = _grad_list(slices)
+    if gl._n and gl.device != out.device:
+        raise ValueError(f"fs_reduce_shard_norm: out is on {out.device}, the slices on {gl.device}")
+    if any(c != FS_BF16 for c in gl.codes) or any(m != n for m in gl.numels):
+        raise ValueError(f"fs_reduce_shard_norm: every slice must be bf16 with {n} elements")
+    need = ctypes.c_int64()
+    _check(lib().fs_reduce_shard_norm_workspace(n, ctypes.byref(need)))
+    _launch(out.device, stream, lib().fs_reduce_shard_norm, n, int(world), int(grad_acc), _dtype_code(reduce_dtype),
+            gl._ptrs, _dev_ptr(out, "out") if n else 0, kind, int(accumulate),
+            _scalar_ptr(total, torch.float64, out.device, "total"),
+            _scalar_ptr(norm, torch.float32, out.device, "norm"), scratch=need.value)
+
+
+def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, grad: torch.Tensor,
+                       param_bf16: Optional[torch.Tensor] = None, *, total: torch.Tensor, max_norm: float,
+                       norm_type=2.0, norm_eps: float = 1e-6, lr: float = 1e-3, beta1: float = 0.9,
+                       beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.01, step: int = 1,
+                       stream=None):
+    """fs_adamw_step on the gradient times min(1, max_norm / (norm_of(total) +
+    norm_eps)), applied as the gradient is read."""
+    kind = _norm_code(norm_type)
+    n = master.numel()
+    for name, t in (("master", master), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
+        if t.dtype != torch.float32 or t.numel() != n:
+            raise ValueError(f"fs_adamw_step_clip: {name} must be float32 with {n} elements")
+    if grad.numel() != n or grad.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("fs_adamw_step_clip: grad must be float32 or bfloat16 with n elements")
+    if param_bf16 is not None and (param_bf16.dtype != torch.bfloat16 or param_bf16.numel() != n):
+        raise ValueError("fs_adamw_step_clip: param_bf16 must be bfloat16 with n elements")
+    dev = master.device
+    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq), ("grad", grad), ("param_bf16", param_bf16)):
+        if t is not None and t.device != dev:
+            raise ValueError(f"fs_adamw_step_clip: {name} is on {t.device}, master on {dev}")
+    hp = AdamWHparams(lr, beta1, beta2, eps, weight_decay, 0, int(step))
+    clip = Clip(_scalar_ptr(total, torch.float64, dev, "total"), max_norm, norm_eps, kind)
+    ptr = (lambda t, w: _dev_ptr(t, w) if n else 0)
+    _launch(dev, stream, lib().fs_adamw_step_clip, n, ptr(master, "master"), ptr(exp_avg, "exp_avg"),
+            ptr(exp_avg_sq, "exp_avg_sq"), ptr(grad, "grad"), FS_BF16 if grad.dtype == torch.bfloat16 else FS_FP32,
+            ptr(param_bf16, "param_bf16") if param_bf16 is not None else None, ctypes.byref(hp), ctypes.byref(clip))
 
 
 def fs_copy_bytes(dst: torch.Tensor, src: torch.Tensor, stream=None):

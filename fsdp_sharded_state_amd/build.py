@@ -3,7 +3,7 @@
     python -m fsdp_sharded_state_amd.build
 
 The library is one hipcc link of the host planner (fs_plan.cpp) and the
-kernels plus launchers (fs_kernels.hip).  Flags:
+kernels plus launchers (fs_kernels.hip, fs_norm.hip).  Flags:
   --offload-arch=gfx950          CDNA4 only, no other targets
   -ffp-contract=off              no FMA contraction: every + and * rounds once,
                                  as the documented update formulas say
@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfsstate.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = [os.path.join(CSRC, "fs_plan.cpp"), os.path.join(CSRC, "fs_kernels.hip")]
+SOURCES = [os.path.join(CSRC, "fs_plan.cpp"), os.path.join(CSRC, "fs_kernels.hip"),
+           os.path.join(CSRC, "fs_norm.hip")]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math",

@@ -33,7 +33,7 @@
 #include <type_traits>
 #include <vector>
 
-#include "fs_device.h"
+#include "fs_norm.h"
 #include "../../include/fs_bench.h"
 
 using namespace fsi;
@@ -857,10 +857,10 @@ __device__ __forceinline__ void store_bf16_group(uint16_t *p, int64_t base, int 
 // three per CU on two of three placements and equal on the third.
 constexpr int kAdamThreads = 64;
 constexpr int64_t kAdamRow = (int64_t)kAdamThreads * 4;   // elements per workgroup
-template <bool GRAD_BF16, bool HAS_P16, bool TAIL>
+template <bool GRAD_BF16, bool HAS_P16, bool CLIP, bool TAIL>
 __device__ __forceinline__ void adamw_group(float *__restrict__ th, float *__restrict__ m, float *__restrict__ v,
                                             const void *__restrict__ grad, uint16_t *__restrict__ p16,
-                                            const AdamConsts &c, int64_t e, int64_t n) {
+                                            const AdamConsts &c, const ClipArgs &clip, int64_t e, int64_t n) {
     const Bounds<1, TAIL> B(e, n);
     if (!B.live(0)) return;
     float G[4], T[4], M[4], V[4];
@@ -874,6 +874,11 @@ __device__ __forceinline__ void adamw_group(float *__restrict__ th, float *__res
     f4(ld16(reinterpret_cast<const char *>(th + e)), T);
     f4(ld16(reinterpret_cast<const char *>(m + e)), M);
     f4(ld16(reinterpret_cast<const char *>(v + e)), V);
+    if (CLIP) {   // the same fp32 product as fs_clip_grads stores
+        const float coef = clip_coef(clip);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[k] = G[k] * coef;
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) adam_elem(c, G[k], T[k], M[k], V[k]);
     store_f32_group<1, TAIL>(th, e, 0, T, B);
@@ -882,25 +887,27 @@ __device__ __forceinline__ void adamw_group(float *__restrict__ th, float *__res
     if (HAS_P16) store_bf16_group<1, TAIL>(p16, e, 0, T, B);
 }
 
-template <bool GRAD_BF16, bool HAS_P16>
+template <bool GRAD_BF16, bool HAS_P16, bool CLIP>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(float *__restrict__ th, float *__restrict__ m,
                                                              float *__restrict__ v, const void *__restrict__ grad,
-                                                             uint16_t *__restrict__ p16, AdamConsts c, int64_t n) {
+                                                             uint16_t *__restrict__ p16, AdamConsts c, ClipArgs clip,
+                                                             int64_t n) {
     const int64_t e = (int64_t)blockIdx.x * kAdamRow + 4 * threadIdx.x;
     if ((int64_t)(blockIdx.x + 1) * kAdamRow <= n)
-        adamw_group<GRAD_BF16, HAS_P16, false>(th, m, v, grad, p16, c, e, n);
+        adamw_group<GRAD_BF16, HAS_P16, CLIP, false>(th, m, v, grad, p16, c, clip, e, n);
     else
-        adamw_group<GRAD_BF16, HAS_P16, true>(th, m, v, grad, p16, c, e, n);
+        adamw_group<GRAD_BF16, HAS_P16, CLIP, true>(th, m, v, grad, p16, c, clip, e, n);
 }
 
 // Element-wise variant for misaligned buffers.
 __global__ __launch_bounds__(kThreads) void adamw_scalar_kernel(int64_t n, float *th, float *m, float *v,
                                                                 const void *grad, int grad_bf16,
-                                                                uint16_t *p16, AdamConsts c) {
+                                                                uint16_t *p16, AdamConsts c, ClipArgs clip) {
     const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (e >= n) return;
-    const float g = grad_bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(grad)[e] << 16)
-                              : reinterpret_cast<const float *>(grad)[e];
+    float g = grad_bf16 ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(grad)[e] << 16)
+                        : reinterpret_cast<const float *>(grad)[e];
+    if (clip.total) g = g * clip_coef(clip);
     float T = th[e], M = m[e], V = v[e];
     adam_elem(c, g, T, M, V);
     th[e] = T;
@@ -1570,6 +1577,47 @@ extern "C" int fs_reduce_shard_ex(int64_t n, int32_t world, int32_t grad_acc, fs
     return FS_OK;
 }
 
+extern "C" int fs_reduce_shard_norm_workspace(int64_t n, int64_t *bytes) {
+    fsi::clear_error();
+    if (!bytes) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: bytes is NULL");
+    if (n < 0) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: n < 0");
+    const fs_dtype f32 = FS_FP32;
+    return fs_grad_norm_workspace(1, &n, &f32, bytes);
+}
+
+extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, fs_dtype reduce_dtype,
+                                    const uint16_t *const *slices, float *out, fs_norm_type type, int32_t accumulate,
+                                    double *total, float *norm, void *workspace, size_t bytes, hipStream_t stream) {
+    fsi::clear_error();
+    const char *what = "fs_reduce_shard_norm";
+    int terms = 0;
+    bool aligned = false, skip = false;
+    if (int rc = check_reduce(what, n, world, grad_acc, slices, out, &terms, &aligned, &skip)) return rc;
+    if (reduce_dtype != FS_BF16 && reduce_dtype != FS_FP32) return fsi::fail(FS_E_DTYPE, "%s: unknown reduce dtype", what);
+    if (reduce_dtype == FS_BF16 && world > kTermsPerPass)
+        return fsi::fail(FS_E_UNSUPPORTED, "%s: bf16 reduce dtype supports world <= %d", what, kTermsPerPass);
+    if (int rc = check_norm_out(what, type, total, norm)) return rc;
+    int64_t need = 0;
+    if (int rc = fs_reduce_shard_norm_workspace(n, &need)) return rc;
+    if (int rc = check_workspace_range(what, workspace, bytes, need, total, norm)) return rc;
+    if (n > 0) {
+        const void *arr[3] = {total, norm, workspace};
+        const int64_t len[3] = {8, norm ? 4 : 0, need};
+        static const char *const name[3] = {"total", "norm", "workspace"};
+        for (int i = 0; i < 3; ++i) {
+            if (ranges_overlap(arr[i], len[i], out, 4 * n)) return fsi::fail(FS_E_INVAL, "%s: %s overlaps out", what, name[i]);
+            for (int t = 0; t < terms; ++t)
+                if (ranges_overlap(arr[i], len[i], slices[t], 2 * n))
+                    return fsi::fail(FS_E_INVAL, "%s: %s overlaps slice %d", what, name[i], t);
+        }
+        if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "%s: n too large for one launch", what);
+    }
+    if (int rc = fs_reduce_shard_ex(n, world, grad_acc, reduce_dtype, slices, out, stream)) return rc;
+    const fs_dtype f32 = FS_FP32;
+    const void *grads = out;
+    return fs_grad_norm(1, &grads, &n, &f32, type, accumulate, total, norm, workspace, bytes, stream);
+}
+
 extern "C" int fs_pack_cast(fs_plan_t plan, const void *const *params, fs_dtype param_dtype, void *out,
                             int32_t rank, hipStream_t stream) {
     fsi::clear_error();
@@ -1609,32 +1657,34 @@ extern "C" int fs_pack_cast(fs_plan_t plan, const void *const *params, fs_dtype 
     return check_launch("fs_pack_cast");
 }
 
-extern "C" int fs_adamw_step(int64_t n, float *master, float *exp_avg, float *exp_avg_sq, const void *grad,
-                             fs_dtype grad_dtype, uint16_t *param_bf16, const fs_adamw_hparams_t *hp,
-                             hipStream_t stream) {
-    fsi::clear_error();
-    if (n < 0) return fsi::fail(FS_E_INVAL, "fs_adamw_step: n < 0");
-    if (int rc = check_hparams("fs_adamw_step", hp)) return rc;
-    if (grad_dtype != FS_BF16 && grad_dtype != FS_FP32) return fsi::fail(FS_E_DTYPE, "fs_adamw_step: unknown grad dtype");
+namespace {
+
+// The step behind both entry points; clip.total is NULL where nothing is clipped.
+int adamw_impl(const char *what, int64_t n, float *master, float *exp_avg, float *exp_avg_sq, const void *grad,
+               fs_dtype grad_dtype, uint16_t *param_bf16, const fs_adamw_hparams_t *hp, const ClipArgs &clip,
+               hipStream_t stream) {
+    if (n < 0) return fsi::fail(FS_E_INVAL, "%s: n < 0", what);
+    if (int rc = check_hparams(what, hp)) return rc;
+    if (grad_dtype != FS_BF16 && grad_dtype != FS_FP32) return fsi::fail(FS_E_DTYPE, "%s: unknown grad dtype", what);
     int64_t nb;
-    if (__builtin_mul_overflow(n, (int64_t)4, &nb)) return fsi::fail(FS_E_OVERFLOW, "fs_adamw_step: n too large");
+    if (__builtin_mul_overflow(n, (int64_t)4, &nb)) return fsi::fail(FS_E_OVERFLOW, "%s: n too large", what);
     if (n == 0) return FS_OK;
-    if (!master || !exp_avg || !exp_avg_sq || !grad) return fsi::fail(FS_E_INVAL, "fs_adamw_step: NULL pointer");
+    if (!master || !exp_avg || !exp_avg_sq || !grad) return fsi::fail(FS_E_INVAL, "%s: NULL pointer", what);
     const int gb = grad_dtype == FS_BF16 ? 2 : 4;
     if (misaligned(master, 4) || misaligned(exp_avg, 4) || misaligned(exp_avg_sq, 4) || misaligned(grad, gb) ||
         (param_bf16 && misaligned(param_bf16, 2)))
-        return fsi::fail(FS_E_ALIGN, "fs_adamw_step: pointer not aligned to its element size");
+        return fsi::fail(FS_E_ALIGN, "%s: pointer not aligned to its element size", what);
     {
-        const void *arr[5] = {master, exp_avg, exp_avg_sq, grad, param_bf16};
-        const int64_t len[5] = {nb, nb, nb, n * gb, param_bf16 ? 2 * n : 0};
-        static const char *const name[5] = {"master", "exp_avg", "exp_avg_sq", "grad", "param_bf16"};
-        const int i = first_overlap(arr, len, 5);
-        if (i >= 0) return fsi::fail(FS_E_INVAL, "fs_adamw_step: %s overlaps another array", name[i]);
+        const void *arr[6] = {master, exp_avg, exp_avg_sq, grad, param_bf16, clip.total};
+        const int64_t len[6] = {nb, nb, nb, n * gb, param_bf16 ? 2 * n : 0, clip.total ? 8 : 0};
+        static const char *const name[6] = {"master", "exp_avg", "exp_avg_sq", "grad", "param_bf16", "total"};
+        const int i = first_overlap(arr, len, 6);
+        if (i >= 0) return fsi::fail(FS_E_INVAL, "%s: %s overlaps another array", what, name[i]);
     }
     const AdamConsts c = adam_consts(*hp);
     const bool aligned = !misaligned(master, 16) && !misaligned(exp_avg, 16) && !misaligned(exp_avg_sq, 16) &&
                          !misaligned(grad, 16) && !(param_bf16 && misaligned(param_bf16, 16));
-    if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "fs_adamw_step: n too large for one launch");
+    if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "%s: n too large for one launch", what);
     (void)hipGetLastError();
     const uint32_t lds = aligned ? lds_cap(kAdamWgsPerCu, (n + kAdamRow - 1) / kAdamRow) : 0;
     for (int64_t off = 0; off < n; off += kAdamSpan) {
@@ -1645,16 +1695,41 @@ extern "C" int fs_adamw_step(int64_t n, float *master, float *exp_avg, float *ex
         if (aligned) {
             const dim3 grid((uint32_t)((len + kAdamRow - 1) / kAdamRow)), b(kAdamThreads);
             with_flags(grad_dtype == FS_BF16, p16 != nullptr, [&](auto grad_bf16, auto has_p16) {
-                hipLaunchKernelGGL((adamw_kernel<decltype(grad_bf16)::value, decltype(has_p16)::value>), grid, b, lds,
-                                   stream, th, m, v, g, p16, c, len);
+                constexpr bool kBf16 = decltype(grad_bf16)::value, kP16 = decltype(has_p16)::value;
+                if (clip.total)
+                    hipLaunchKernelGGL((adamw_kernel<kBf16, kP16, true>), grid, b, lds, stream, th, m, v, g, p16, c,
+                                       clip, len);
+                else
+                    hipLaunchKernelGGL((adamw_kernel<kBf16, kP16, false>), grid, b, lds, stream, th, m, v, g, p16, c,
+                                       clip, len);
             });
         } else {
             hipLaunchKernelGGL(adamw_scalar_kernel, dim3((uint32_t)((len + kThreads - 1) / kThreads)), dim3(kThreads),
-                               0, stream, len, th, m, v, g, (int)(grad_dtype == FS_BF16), p16, c);
+                               0, stream, len, th, m, v, g, (int)(grad_dtype == FS_BF16), p16, c, clip);
         }
-        if (int rc = check_launch("fs_adamw_step")) return rc;
+        if (int rc = check_launch(what)) return rc;
     }
     return FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_adamw_step(int64_t n, float *master, float *exp_avg, float *exp_avg_sq, const void *grad,
+                             fs_dtype grad_dtype, uint16_t *param_bf16, const fs_adamw_hparams_t *hp,
+                             hipStream_t stream) {
+    fsi::clear_error();
+    return adamw_impl("fs_adamw_step", n, master, exp_avg, exp_avg_sq, grad, grad_dtype, param_bf16, hp, ClipArgs{},
+                      stream);
+}
+
+extern "C" int fs_adamw_step_clip(int64_t n, float *master, float *exp_avg, float *exp_avg_sq, const void *grad,
+                                  fs_dtype grad_dtype, uint16_t *param_bf16, const fs_adamw_hparams_t *hp,
+                                  const fs_clip_t *clip, hipStream_t stream) {
+    fsi::clear_error();
+    ClipArgs c;
+    if (int rc = check_clip("fs_adamw_step_clip", clip, &c)) return rc;
+    return adamw_impl("fs_adamw_step_clip", n, master, exp_avg, exp_avg_sq, grad, grad_dtype, param_bf16, hp, c,
+                      stream);
 }
 
 namespace {

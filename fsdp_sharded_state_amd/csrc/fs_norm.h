@@ -1,0 +1,78 @@
+// fs_norm.h -- the gradient norm's "total" as the kernels of both HIP sources
+// make and use it.  Not part of the public ABI.
+//
+// The total is one double: the sum of squares (FS_NORM_L2) or the largest
+// magnitude (FS_NORM_INF) of a set of gradients.  It is exact enough to be
+// added up over calls, groups and ranks in any order: the square of a bf16 or
+// fp32 value is exact in a double and cannot overflow it, so a total of n
+// values is off by at most (n + joins) * 2^-53 relative, whatever the order,
+// and in fact far less.  Every kernel writes its partial totals to fixed
+// places of a workspace, and one workgroup joins them in a fixed order, so a
+// call's result does not depend on which workgroup ends first.
+#pragma once
+#include "fs_device.h"
+
+namespace fsi {
+
+enum NormKind { kNoNorm = 0, kL2 = FS_NORM_L2, kInf = FS_NORM_INF };
+
+// Join two partial totals.  The larger magnitude, with NaN above everything.
+template <int KIND>
+__device__ __forceinline__ double norm_join(double a, double b) {
+    if (KIND == kL2) return a + b;
+    return a != a || a > b ? a : b;   // b if it is NaN: a > NaN is false
+}
+
+// One value's share of the total, added to t.  The square is exact (48
+// significant bits), so the fused multiply-add rounds only the sum.
+template <int KIND>
+__device__ __forceinline__ double norm_add(double t, float x) {
+    if (KIND == kL2) {
+        const double d = x;
+        return fma(d, d, t);
+    }
+    return norm_join<KIND>(t, (double)fabsf(x));
+}
+
+// The workgroup's total, in thread 0 (the other threads get parts of it).
+// `lds`: one double per wave.  A fixed tree: the same for every launch.
+template <int KIND, int THREADS>
+__device__ __forceinline__ double norm_block_join(double t, double *lds) {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) t = norm_join<KIND>(t, __shfl_down(t, d));
+    if constexpr (THREADS > 64) {
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = t;
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int w = 1; w < THREADS / 64; ++w) t = norm_join<KIND>(t, lds[w]);
+    }
+    return t;
+}
+
+// What a consumer needs of fs_clip_t, by value.
+struct ClipArgs {
+    const double *total;
+    double max_norm, eps;
+    int32_t inf;
+};
+
+__device__ __forceinline__ double norm_of(double total, int inf) { return inf ? total : sqrt(total); }
+
+// min(1, max_norm / (norm + eps)), computed in double and rounded once.  A
+// norm within the limit gives exactly 1; a NaN norm gives NaN, an infinite
+// one 0 (or 1 where max_norm is infinite too).
+__device__ __forceinline__ float clip_coef(const ClipArgs &c) {
+    const double d = norm_of(c.total[0], c.inf) + c.eps;
+    return d <= c.max_norm ? 1.0f : (float)(c.max_norm / d);
+}
+
+// ------------------------------------------------------------ host side --
+
+int check_norm_out(const char *what, int type, const double *total, const float *norm);
+int check_clip(const char *what, const fs_clip_t *clip, ClipArgs *out);
+int check_workspace_range(const char *what, const void *workspace, size_t bytes, int64_t need, const double *total,
+                          const float *norm);
+int launch_norm_finish(const char *what, int type, int accumulate, const double *parts, int64_t count, double *total,
+                       float *norm, hipStream_t stream);
+
+}  // namespace fsi

@@ -1,0 +1,393 @@
+// fs_norm.hip -- gfx950 (CDNA4) kernels of the gradient norm over many
+// tensors and of clipping them in place, and their C-ABI launchers.
+//
+// Both are HBM-bound streams over a list of tensors: the norm reads every
+// element once (2 or 4 bytes), the clip reads and writes it once.  A list is
+// cut into tiles of 16-byte blocks, each inside one tensor; the list itself
+// (addresses, sizes, tile counts) travels in the kernel arguments, so a call
+// copies nothing to the GPU and can be captured into a graph, and kListMax
+// tensors fit one launch.  Tensors start on any element (views of a flat
+// shard): a tile is made of the aligned 16-byte blocks that overlap the
+// tensor, and the elements of its first and last block that lie outside are
+// masked.  Such a block never crosses a page, so only mapped memory is read.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "fs_norm.h"
+
+using namespace fsi;
+
+namespace {
+
+constexpr int kListMax = 192;   // tensors of one launch: the list takes 3840 of the 4096 argument bytes
+
+struct ListArgs {
+    char *ptr[kListMax];            // first element
+    int64_t size[kListMax];         // bytes * 2, + 1 for fp32
+    uint32_t tile_end[kListMax];    // tiles of this tensor and those before it
+};
+
+// A tile's place: blocks [first, first + nblk) of the tensor whose bytes are
+// [lo, hi) from the aligned address `base`.
+struct TileAt {
+    char *base;
+    int64_t first, lo, hi;
+    int nblk;
+    bool f32, whole;   // whole: no element of any of the blocks lies outside the tensor
+};
+
+template <int TILE>
+__device__ __forceinline__ TileAt tile_at(const ListArgs &L, int count, uint32_t tile) {
+    int a = 0, b = count - 1;   // the first tensor whose tile_end lies above `tile`
+    while (a < b) {
+        const int mid = (a + b) >> 1;
+        if (L.tile_end[mid] <= tile) a = mid + 1; else b = mid;
+    }
+    const uint32_t before = a ? L.tile_end[a - 1] : 0;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(L.ptr[a]);
+    const int64_t size = L.size[a];
+    TileAt t;
+    t.f32 = size & 1;
+    t.lo = (int64_t)(p & 15);
+    t.hi = t.lo + (size >> 1);
+    t.base = reinterpret_cast<char *>(p - (uintptr_t)t.lo);
+    t.first = (int64_t)(tile - before) * TILE;
+    t.nblk = (int)imin(TILE, ((t.hi + 15) >> 4) - t.first);
+    t.whole = 16 * t.first >= t.lo && 16 * (t.first + t.nblk) <= t.hi;
+    return t;
+}
+
+// Elements [*e_lo, *e_hi) of block b (of the tensor) lie inside the tensor.
+template <int W>
+__device__ __forceinline__ void block_range(const TileAt &t, int64_t b, int *e_lo, int *e_hi) {
+    *e_lo = (int)imax(0, (t.lo - 16 * b) / W);
+    *e_hi = (int)imin(16 / W, (t.hi - 16 * b) / W);
+}
+
+// ------------------------------------------------------------------ norm --
+
+constexpr int kNormUnroll = 8;                            // 16-byte blocks in flight per lane
+constexpr int kNormTile = kThreads * kNormUnroll;         // blocks of a tile (32 KB)
+constexpr int kNormWgs = 2048;                            // workgroups of a launch: each walks its share of the tiles
+
+// bf16 lanes as fp32 bits
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+template <int KIND, int W>
+__device__ __forceinline__ double block_total(double t, u32x4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (W == 4) {
+            t = norm_add<KIND>(t, __uint_as_float(w[i]));
+        } else {
+            t = norm_add<KIND>(t, bf_lo(w[i]));
+            t = norm_add<KIND>(t, bf_hi(w[i]));
+        }
+    }
+    return t;
+}
+
+template <int KIND, int W>
+__device__ __forceinline__ double tile_total(double t, const TileAt &at) {
+    u32x4 v[kNormUnroll];
+#pragma unroll
+    for (int u = 0; u < kNormUnroll; ++u) {
+        const int b = u * kThreads + threadIdx.x;
+        v[u] = u32x4{0u, 0u, 0u, 0u};   // zeros add nothing to either total
+        if (b < at.nblk) {
+            v[u] = ld16(at.base + 16 * (at.first + b));
+            if (!at.whole) {
+                int e_lo, e_hi;
+                block_range<W>(at, at.first + b, &e_lo, &e_hi);
+                v[u] &= elem_mask<W>(e_lo, e_hi);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kNormUnroll; ++u) t = block_total<KIND, W>(t, v[u]);
+    return t;
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void list_norm_kernel(ListArgs L, int count, uint32_t ntiles, double *parts) {
+    __shared__ double lds[kThreads / 64];
+    double t = 0;
+    for (uint32_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
+        const TileAt at = tile_at<kNormTile>(L, count, tile);
+        t = at.f32 ? tile_total<KIND, 4>(t, at) : tile_total<KIND, 2>(t, at);
+    }
+    t = norm_block_join<KIND, kThreads>(t, lds);
+    if (threadIdx.x == 0) parts[blockIdx.x] = t;
+}
+
+// Joins the partial totals in a fixed order; writes the total (joined to the
+// one that stands there, where the call accumulates) and the norm.
+constexpr int kFinishThreads = 1024;
+
+template <int KIND>
+__global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(const double *__restrict__ parts, int64_t count,
+                                                                     int accumulate, double *total, float *norm) {
+    __shared__ double lds[kFinishThreads / 64];
+    double t = 0;
+    for (int64_t i = threadIdx.x; i < count; i += kFinishThreads) t = norm_join<KIND>(t, parts[i]);
+    t = norm_block_join<KIND, kFinishThreads>(t, lds);
+    if (threadIdx.x == 0) {
+        if (accumulate) t = norm_join<KIND>(total[0], t);
+        total[0] = t;
+        if (norm) norm[0] = (float)norm_of(t, KIND == kInf);
+    }
+}
+
+// ------------------------------------------------------------------ clip --
+
+constexpr int kClipUnroll = 4;
+constexpr int kClipTile = kThreads * kClipUnroll;   // blocks of a tile (16 KB): one per workgroup
+
+template <int W>
+__device__ __forceinline__ u32x4 scale_block(u32x4 v, float c) {
+    if (W == 4)
+        return u32x4{__float_as_uint(__uint_as_float(v.x) * c), __float_as_uint(__uint_as_float(v.y) * c),
+                     __float_as_uint(__uint_as_float(v.z) * c), __float_as_uint(__uint_as_float(v.w) * c)};
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = (uint32_t)bf16_rne_bits(__float_as_uint(bf_lo(w[i]) * c)) |
+               ((uint32_t)bf16_rne_bits(__float_as_uint(bf_hi(w[i]) * c)) << 16);
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
+template <int W>
+__device__ __forceinline__ void clip_tile(const TileAt &at, float c) {
+    u32x4 v[kClipUnroll];
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+        const int b = u * kThreads + threadIdx.x;
+        if (b < at.nblk) v[u] = ld16(at.base + 16 * (at.first + b));
+    }
+#pragma unroll
+    for (int u = 0; u < kClipUnroll; ++u) {
+        const int b = u * kThreads + threadIdx.x;
+        if (b >= at.nblk) continue;
+        char *p = at.base + 16 * (at.first + b);
+        const u32x4 x = scale_block<W>(v[u], c);
+        int e_lo = 0, e_hi = 16 / W;
+        if (!at.whole) block_range<W>(at, at.first + b, &e_lo, &e_hi);
+        if (e_lo == 0 && e_hi == 16 / W)
+            st16(p, x);
+        else
+            store_elems<W>(p, x, e_lo, e_hi);   // a neighbour in the same block may belong to another tensor
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void list_clip_kernel(ListArgs L, int count, ClipArgs clip, float *norm) {
+    const float c = clip_coef(clip);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)norm_of(clip.total[0], clip.inf);
+    if (c == 1.0f || count == 0) return;   // times one: the gradients stay as they are, unread
+    const TileAt at = tile_at<kClipTile>(L, count, blockIdx.x);
+    if (at.f32) clip_tile<4>(at, c); else clip_tile<2>(at, c);
+}
+
+// -------------------------------------------------------------- launchers --
+
+int elem_bytes(fs_dtype d) { return d == FS_BF16 ? 2 : 4; }
+
+// Tiles of `tile` 16-byte blocks that cover nb > 0 bytes at p.
+int64_t tiles_of(const void *p, int64_t nb, int tile) {
+    const int64_t blocks = ((int64_t)(reinterpret_cast<uintptr_t>(p) & 15) + nb + 15) >> 4;
+    return (blocks + tile - 1) / tile;
+}
+
+// Shared argument checks of the list calls, whose tiles are of `tile` blocks.
+int check_list(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
+               const fs_dtype *dtypes, int tile, const void *total, const void *norm) {
+    int64_t tiles = 0;
+    if (n_tensors < 0) return fail(FS_E_INVAL, "%s: n_tensors < 0", what);
+    if (n_tensors > 0 && (!grads || !numel || !dtypes)) return fail(FS_E_INVAL, "%s: NULL list", what);
+    for (int i = 0; i < n_tensors; ++i) {
+        if (numel[i] < 0) return fail(FS_E_INVAL, "%s: tensor %d has a negative element count", what, i);
+        if (dtypes[i] != FS_BF16 && dtypes[i] != FS_FP32) return fail(FS_E_DTYPE, "%s: tensor %d has an unknown dtype", what, i);
+        if (numel[i] > (INT64_MAX >> 4)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large", what, i);
+        if (numel[i] == 0) continue;
+        const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
+        if (!grads[i]) return fail(FS_E_INVAL, "%s: tensor %d is NULL", what, i);
+        if (misaligned(grads[i], elem_bytes(dtypes[i])))
+            return fail(FS_E_ALIGN, "%s: tensor %d not aligned to its element size", what, i);
+        tiles += tiles_of(grads[i], nb, tile);
+        if (tiles > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+        if (ranges_overlap(total, 8, grads[i], nb) || (norm && ranges_overlap(norm, 4, grads[i], nb)))
+            return fail(FS_E_INVAL, "%s: total or norm overlaps tensor %d", what, i);
+    }
+    return FS_OK;
+}
+
+// Cut the list into launches of at most kListMax tensors and call
+// f(args, tensors, tiles) for each; tensors without elements are left out.
+template <int TILE, class F>
+void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes, F &&f) {
+    ListArgs L;
+    int count = 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        if (numel[i] == 0) continue;
+        if (count == kListMax) {
+            f(L, count, (uint32_t)tiles);
+            count = 0;
+            tiles = 0;
+        }
+        const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
+        tiles += tiles_of(grads[i], nb, TILE);
+        L.ptr[count] = static_cast<char *>(const_cast<void *>(grads[i]));
+        L.size[count] = nb * 2 + (dtypes[i] == FS_FP32);
+        L.tile_end[count++] = (uint32_t)tiles;
+    }
+    if (count) f(L, count, (uint32_t)tiles);
+}
+
+// Two tensors that share memory would be scaled twice, or raced on.
+int check_disjoint(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
+                   const fs_dtype *dtypes) {
+    struct Range { uintptr_t lo, hi; };
+    try {
+        std::vector<Range> r;
+        r.reserve((size_t)n_tensors);
+        for (int i = 0; i < n_tensors; ++i)
+            if (numel[i] > 0) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]);
+                r.push_back({a, a + (uintptr_t)(numel[i] * elem_bytes(dtypes[i]))});
+            }
+        std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
+        for (size_t i = 1; i < r.size(); ++i)
+            if (r[i].lo < r[i - 1].hi) return fail(FS_E_INVAL, "%s: two tensors share memory", what);
+    } catch (const std::bad_alloc &) {
+        return fail(FS_E_NOMEM, "%s: out of host memory", what);
+    }
+    return FS_OK;
+}
+
+}  // namespace
+
+namespace fsi {
+
+int check_norm_out(const char *what, int type, const double *total, const float *norm) {
+    if (type != FS_NORM_L2 && type != FS_NORM_INF) return fail(FS_E_UNSUPPORTED, "%s: unknown norm type %d", what, type);
+    if (!total) return fail(FS_E_INVAL, "%s: total is NULL", what);
+    if (misaligned(total, 8) || misaligned(norm, 4))
+        return fail(FS_E_ALIGN, "%s: total or norm not aligned to its element size", what);
+    if (norm && ranges_overlap(total, 8, norm, 4)) return fail(FS_E_INVAL, "%s: norm overlaps total", what);
+    return FS_OK;
+}
+
+int check_clip(const char *what, const fs_clip_t *clip, ClipArgs *out) {
+    if (!clip) return fail(FS_E_INVAL, "%s: clip is NULL", what);
+    if (int rc = check_norm_out(what, clip->norm_type, clip->total, nullptr)) return rc;
+    if (!(clip->max_norm >= 0.f)) return fail(FS_E_INVAL, "%s: max_norm must be >= 0", what);
+    if (!(clip->eps >= 0.f) || isinf(clip->eps)) return fail(FS_E_INVAL, "%s: eps must be >= 0 and finite", what);
+    *out = ClipArgs{clip->total, clip->max_norm, clip->eps, clip->norm_type == FS_NORM_INF};
+    return FS_OK;
+}
+
+int check_workspace_range(const char *what, const void *workspace, size_t bytes, int64_t need, const double *total,
+                          const float *norm) {
+    if (need == 0) return FS_OK;
+    if (!workspace) return fail(FS_E_INVAL, "%s: workspace is NULL", what);
+    if (misaligned(workspace, 8)) return fail(FS_E_ALIGN, "%s: workspace not 8-byte aligned", what);
+    if ((int64_t)bytes < need)
+        return fail(FS_E_INVAL, "%s: workspace too small (%zu < %lld bytes)", what, bytes, (long long)need);
+    if (ranges_overlap(workspace, need, total, 8) || (norm && ranges_overlap(workspace, need, norm, 4)))
+        return fail(FS_E_INVAL, "%s: workspace overlaps total or norm", what);
+    return FS_OK;
+}
+
+int launch_norm_finish(const char *what, int type, int accumulate, const double *parts, int64_t count, double *total,
+                       float *norm, hipStream_t stream) {
+    if (type == FS_NORM_L2)
+        hipLaunchKernelGGL(norm_finish_kernel<kL2>, dim3(1), dim3(kFinishThreads), 0, stream, parts, count, accumulate,
+                           total, norm);
+    else
+        hipLaunchKernelGGL(norm_finish_kernel<kInf>, dim3(1), dim3(kFinishThreads), 0, stream, parts, count,
+                           accumulate, total, norm);
+    return check_launch(what);
+}
+
+}  // namespace fsi
+
+extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, const fs_dtype *dtypes,
+                                      int64_t *bytes) {
+    clear_error();
+    if (!bytes) return fail(FS_E_INVAL, "fs_grad_norm_workspace: bytes is NULL");
+    if (n_tensors < 0) return fail(FS_E_INVAL, "fs_grad_norm_workspace: n_tensors < 0");
+    if (n_tensors > 0 && (!numel || !dtypes)) return fail(FS_E_INVAL, "fs_grad_norm_workspace: NULL list");
+    *bytes = ((int64_t)n_tensors + kListMax - 1) / kListMax * kNormWgs * (int64_t)sizeof(double);
+    return FS_OK;
+}
+
+namespace {
+
+int check_grad_norm(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
+                    const fs_dtype *dtypes, fs_norm_type type, const double *total, const float *norm,
+                    const void *workspace, size_t bytes) {
+    if (int rc = check_norm_out(what, type, total, norm)) return rc;
+    if (int rc = check_list(what, n_tensors, grads, numel, dtypes, kNormTile, total, norm)) return rc;
+    int64_t need = 0;
+    if (int rc = fs_grad_norm_workspace(n_tensors, numel, dtypes, &need)) return rc;
+    if (int rc = check_workspace_range(what, workspace, bytes, need, total, norm)) return rc;
+    for (int i = 0; i < n_tensors; ++i)
+        if (ranges_overlap(workspace, need, grads[i], numel[i] * elem_bytes(dtypes[i])))
+            return fail(FS_E_INVAL, "%s: workspace overlaps tensor %d", what, i);
+    return FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_grad_norm(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes,
+                            fs_norm_type type, int32_t accumulate, double *total, float *norm, void *workspace,
+                            size_t bytes, hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_grad_norm";
+    if (int rc = check_grad_norm(what, n_tensors, grads, numel, dtypes, type, total, norm, workspace, bytes)) return rc;
+    (void)hipGetLastError();
+    double *parts = static_cast<double *>(workspace);
+    int64_t count = 0;
+    for_each_launch<kNormTile>(n_tensors, grads, numel, dtypes, [&](const ListArgs &L, int tensors, uint32_t tiles) {
+        const uint32_t grid = std::min<uint32_t>(kNormWgs, tiles);
+        if (type == FS_NORM_L2)
+            hipLaunchKernelGGL(list_norm_kernel<kL2>, dim3(grid), dim3(kThreads), 0, stream, L, tensors, tiles,
+                               parts + count);
+        else
+            hipLaunchKernelGGL(list_norm_kernel<kInf>, dim3(grid), dim3(kThreads), 0, stream, L, tensors, tiles,
+                               parts + count);
+        count += grid;
+    });
+    if (int rc = check_launch(what)) return rc;
+    return launch_norm_finish(what, type, accumulate != 0, parts, count, total, norm, stream);
+}
+
+extern "C" int fs_clip_grads(int32_t n_tensors, void *const *grads, const int64_t *numel, const fs_dtype *dtypes,
+                             const fs_clip_t *clip, float *norm, hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_clip_grads";
+    ClipArgs c;
+    if (int rc = check_clip(what, clip, &c)) return rc;
+    if (int rc = check_norm_out(what, clip->norm_type, clip->total, norm)) return rc;
+    if (int rc = check_list(what, n_tensors, grads, numel, dtypes, kClipTile, clip->total, norm)) return rc;
+    if (int rc = check_disjoint(what, n_tensors, grads, numel, dtypes)) return rc;
+    (void)hipGetLastError();
+    float *out = norm;   // the first launch writes it
+    for_each_launch<kClipTile>(n_tensors, grads, numel, dtypes, [&](const ListArgs &L, int tensors, uint32_t tiles) {
+        hipLaunchKernelGGL(list_clip_kernel, dim3(tiles), dim3(kThreads), 0, stream, L, tensors, c, out);
+        out = nullptr;
+    });
+    if (out) {   // no tensor has elements
+        ListArgs none;
+        memset(&none, 0, sizeof none);
+        hipLaunchKernelGGL(list_clip_kernel, dim3(1), dim3(kThreads), 0, stream, none, 0, c, out);
+    }
+    return check_launch(what);
+}

@@ -75,6 +75,11 @@ typedef enum {
     FS_FSDP2_PER_PARAM = 2  /* each parameter chunked on dim 0          [FvF section 03] */
 } fs_mode;
 
+typedef enum {
+    FS_NORM_L2 = 1, /* the total is the sum of squares, the norm its square root */
+    FS_NORM_INF = 2 /* the total is the largest magnitude, which is the norm */
+} fs_norm_type;
+
 typedef struct fs_plan_s *fs_plan_t;       /* opaque; host memory owned by the library */
 typedef struct fs_reshard_s *fs_reshard_t; /* opaque; host memory owned by the library */
 
@@ -450,6 +455,118 @@ int fs_reduce_adamw_step_noalloc(int64_t n, int32_t world, int32_t grad_acc,
                                  const uint16_t *const *slices, float *master,
                                  float *exp_avg, float *exp_avg_sq, uint16_t *param_bf16,
                                  const fs_adamw_hparams_t *hp, hipStream_t stream);
+
+/*
+ * Gradient clipping.  The source pages' recipe has no clipping; these calls
+ * follow the usual definition: with the global norm of all gradients,
+ *   coef = min(1, max_norm / (norm + eps)),  g <- g * coef.
+ * What the calls pass on is the `total`, one double in device memory: the sum
+ * of squares of the gradients (FS_NORM_L2) or their largest magnitude
+ * (FS_NORM_INF).  Totals of several calls, groups or ranks join by adding
+ * them up (L2) or taking the largest (INF); an all-reduce of 8 bytes makes
+ * the total of all ranks' shards.  The calls that clip take the coefficient
+ * from the total on the GPU, so no step waits for the host:
+ *   fs_reduce_shard_norm (per group, accumulating) -> all-reduce of the total
+ *   -> fs_adamw_step_clip.
+ * Squares are exact and sums are held in double: a total neither overflows
+ * nor loses small gradients, and it is the same for every run of the same
+ * call (partial totals are joined in a fixed order).  NaN and infinite
+ * gradients show in the total; pads are zero and add nothing.
+ */
+
+/* How the gradients are clipped. */
+typedef struct {
+    const double *total;    /* device: the total of all gradients, 8-byte aligned */
+    float max_norm;         /* >= 0; infinite: never clip */
+    float eps;              /* >= 0, finite; the usual value is 1e-6 */
+    fs_norm_type norm_type; /* what the total is */
+} fs_clip_t;
+
+/*
+ * fs_grad_norm -- total and norm of a list of gradient tensors.
+ *
+ *   n_tensors        >= 0.
+ *   grads   (host)   n_tensors device pointers, each aligned to its element
+ *                    size (a view of a flat shard may start on any element);
+ *                    tensors may overlap.  Those without elements may be NULL.
+ *   numel   (host)   element counts, >= 0.
+ *   dtypes  (host)   element types, FS_BF16 or FS_FP32; a list may mix them.
+ *   type             FS_NORM_L2 or FS_NORM_INF.
+ *   accumulate       0: total is written (an empty list gives 0); else the
+ *                    list's total is joined to the one that stands there.
+ *   total  (device)  one double.
+ *   norm   (device)  one fp32, or NULL: also receives the norm of the total
+ *                    written (infinite where it is beyond fp32; the total is
+ *                    what clipping goes by).
+ *   workspace (device) the bytes that fs_grad_norm_workspace gives, 8-byte
+ *                    aligned, of any content; NULL where it gives 0.  Calls
+ *                    that overlap in time need a workspace each.
+ * Errors: FS_E_INVAL (negative counts, NULL pointers, workspace too small,
+ * total, norm or workspace overlapping each other or a tensor), FS_E_DTYPE,
+ * FS_E_UNSUPPORTED (another norm type), FS_E_ALIGN, FS_E_OVERFLOW, FS_E_HIP.
+ */
+int fs_grad_norm(int32_t n_tensors, const void *const *grads, const int64_t *numel,
+                 const fs_dtype *dtypes, fs_norm_type type, int32_t accumulate,
+                 double *total, float *norm, void *workspace, size_t bytes,
+                 hipStream_t stream);
+
+/* fs_grad_norm_workspace -- the workspace bytes of that call into *bytes (host). */
+int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, const fs_dtype *dtypes,
+                           int64_t *bytes);
+
+/*
+ * fs_clip_grads -- scale a list of gradient tensors in place by the clip's
+ * coefficient: fp32 elements by one fp32 product, bf16 elements by an fp32
+ * product rounded to nearest even.  A coefficient of exactly 1 leaves them
+ * unread.
+ *
+ *   n_tensors, grads, numel, dtypes: as fs_grad_norm; tensors may not overlap.
+ *   clip   (host)    see fs_clip_t.  The coefficient is computed in double
+ *                    and rounded once to fp32; it is 1 for a norm + eps of at
+ *                    most max_norm, and NaN for a NaN norm.
+ *   norm   (device)  one fp32, or NULL: receives the norm of the total.
+ * Errors: as fs_grad_norm; FS_E_INVAL also for max_norm or eps out of range
+ * and tensors that share memory; FS_E_NOMEM.
+ */
+int fs_clip_grads(int32_t n_tensors, void *const *grads, const int64_t *numel,
+                  const fs_dtype *dtypes, const fs_clip_t *clip, float *norm,
+                  hipStream_t stream);
+
+/*
+ * fs_reduce_shard_norm -- fs_reduce_shard_ex, and the total and norm of the
+ * averaged gradients it writes, of which each is squared as stored.
+ *
+ *   n, world, grad_acc, reduce_dtype, slices, out: as fs_reduce_shard_ex; out
+ *                    is the same bit for bit.
+ *   type, accumulate, total, norm: as fs_grad_norm.
+ *   workspace (device) the bytes that fs_reduce_shard_norm_workspace gives
+ *                    for n; as fs_grad_norm's.
+ * Errors: those of fs_reduce_shard_ex and fs_grad_norm.
+ */
+int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, fs_dtype reduce_dtype,
+                         const uint16_t *const *slices, float *out, fs_norm_type type,
+                         int32_t accumulate, double *total, float *norm, void *workspace,
+                         size_t bytes, hipStream_t stream);
+
+/* fs_reduce_shard_norm_workspace -- the workspace bytes of that call into *bytes (host). */
+int fs_reduce_shard_norm_workspace(int64_t n, int64_t *bytes);
+
+/*
+ * fs_adamw_step_clip -- fs_adamw_step on the clipped gradient: every gradient
+ * is multiplied by the clip's coefficient in fp32 as it is read; the gradient
+ * array stays as it is.  With fp32 gradients theta, m, v and param_bf16 are
+ * bit-identical to fs_clip_grads followed by fs_adamw_step; bf16 gradients
+ * are not rounded to bf16 in between.
+ *
+ *   clip   (host)    see fs_clip_t and fs_clip_grads.
+ *   other arguments as fs_adamw_step.
+ * Errors: those of fs_adamw_step; those of fs_clip_grads for clip; FS_E_INVAL
+ * also for a total inside one of the arrays.
+ */
+int fs_adamw_step_clip(int64_t n, float *master, float *exp_avg, float *exp_avg_sq,
+                       const void *grad, fs_dtype grad_dtype, uint16_t *param_bf16,
+                       const fs_adamw_hparams_t *hp, const fs_clip_t *clip,
+                       hipStream_t stream);
 
 /* fs_last_error -- message for the calling thread's last failed call
  * (empty string if none).  The pointer stays valid until the next call. */
