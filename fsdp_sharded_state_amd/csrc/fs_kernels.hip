@@ -485,12 +485,24 @@ __device__ __forceinline__ u32x4 ld_slice16(const uint16_t *p, int64_t off) {
     return funnel16(lo, hi, sh);
 }
 
+// Lane 0 writes its wave's partial total.  One per wave, with no barrier: at
+// one to three workgroups per CU the waves of a workgroup should not wait for
+// each other.
+template <int KIND>
+__device__ __forceinline__ void store_wave_total(double t, double *__restrict__ parts) {
+    t = norm_wave_join<KIND>(t);
+    if ((threadIdx.x & 63) == 0) parts[(int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = t;
+}
+
 // Misaligned slices or output: lane i owns 8 consecutive elements, one
 // funnel-shifted 16-byte load per term, element stores; the last n % 8
 // elements go one per lane of the first wave.
+template <int KIND>
 __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, int nterms, int first_pass,
                                                                   int last_pass, float world, int64_t n,
-                                                                  float *__restrict__ out) {
+                                                                  float *__restrict__ out,
+                                                                  double *__restrict__ parts) {
+    double total = 0;
     const int64_t nvec = n >> 3;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i < nvec) {
@@ -518,6 +530,10 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[8 * i + e] = acc[e];
+        if (KIND) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) total = norm_add<KIND>(total, acc[e]);
+        }
     }
     const int64_t tail = n - nvec * 8;
     if (blockIdx.x == 0 && (int64_t)threadIdx.x < tail) {
@@ -531,8 +547,11 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
             acc = out[e];
         }
         for (; t < nterms; ++t) acc = acc + __uint_as_float((uint32_t)sa.p[t][e] << 16);
-        out[e] = last_pass ? acc / world : acc;
+        if (last_pass) acc = acc / world;
+        out[e] = acc;
+        if (KIND) total = norm_add<KIND>(total, acc);
     }
+    if (KIND) store_wave_total<KIND>(total, parts);
 }
 
 constexpr int kRedGroupsMany = 16;                                      // passes of > kRedFewTerms terms
@@ -621,6 +640,18 @@ __device__ __forceinline__ void store_f32_group(float *p, int64_t base, int u, c
     }
 }
 
+// The total of the lane's G groups (the elements below n), added to t.
+template <int KIND, int G, bool TAIL>
+__device__ __forceinline__ double groups_total(double t, const float *v, int64_t base, const Bounds<G, TAIL> &B) {
+#pragma unroll
+    for (int u = 0; u < G; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!TAIL || base + u * kWgRow + k < B.n) t = norm_add<KIND>(t, v[4 * u + k]);
+    }
+    return t;
+}
+
 // Sum the lane's G groups over slices 0..nterms-1 in slice order, into acc
 // (init: acc starts as slice 0 itself, so -0 survives; else slice 0 is added
 // to acc).  SL slices are in flight: slot k % SL holds slice k, refilled with
@@ -651,9 +682,10 @@ __device__ __forceinline__ void sum_slices(const SliceArgs &sa, int nterms, bool
     }
 }
 
-template <int G, bool TAIL>
+template <int KIND, int G, bool TAIL>
 __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, int first_pass, int last_pass,
-                                             float world, float *__restrict__ out, int64_t base, int64_t n) {
+                                             float world, float *__restrict__ out, double &norm_total,
+                                             int64_t base, int64_t n) {
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G];
     if (!first_pass) load_f32_groups<G, G, TAIL>(acc, out, base, B);   // partial sums of the earlier passes
@@ -664,6 +696,7 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
     }
 #pragma unroll
     for (int u = 0; u < G; ++u) store_f32_group<G, TAIL>(out, base, u, acc + 4 * u, B);
+    if (KIND) norm_total = groups_total<KIND>(norm_total, acc, base, B);
 }
 
 // The chunk of workgroup blockIdx.x: whole, or the last one cut by n (walked
@@ -683,13 +716,19 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
         }                                                                                       \
     } while (0)
 
-template <int G>
+// KIND: kNoNorm, or (in the last pass) the norm whose partial totals, one per
+// wave, go to `parts`.
+template <int KIND, int G>
 __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, int nterms, int first_pass,
                                                                 int last_pass, float world,
-                                                                float *__restrict__ out, int64_t n) {
+                                                                float *__restrict__ out, int64_t n,
+                                                                double *__restrict__ parts) {
     static_assert(G % kTailGroups == 0, "the tail walks whole sub-chunks");
-    FS_CHUNK_DISPATCH(G, (reduce_chunk<G, false>(sa, nterms, first_pass, last_pass, world, out, base, n)),
-                      (reduce_chunk<kTailGroups, true>(sa, nterms, first_pass, last_pass, world, out, base, n)));
+    double t = 0;
+    FS_CHUNK_DISPATCH(G, (reduce_chunk<KIND, G, false>(sa, nterms, first_pass, last_pass, world, out, t, base, n)),
+                      (reduce_chunk<KIND, kTailGroups, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
+                                                             n)));
+    if (KIND) store_wave_total<KIND>(t, parts);
 }
 
 // ------------------------------------------------- bf16 reduce dtype --
@@ -710,9 +749,10 @@ __device__ __forceinline__ float bf16_round_f32(float f) {
     return __uint_as_float((uint32_t)bf16_rne_bits(__float_as_uint(f)) << 16);
 }
 
-template <int G, bool TAIL>
+template <int KIND, int G, bool TAIL>
 __device__ __forceinline__ void reduce_rs_chunk(const SliceArgs &sa, int nsteps, int world, int first_pass,
-                                                float worldf, float *__restrict__ out, int64_t base, int64_t n) {
+                                                float worldf, float *__restrict__ out, double &norm_total,
+                                                int64_t base, int64_t n) {
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G], sum[4 * G];
     u32x2 xa[G], xb[G];
@@ -756,21 +796,29 @@ __device__ __forceinline__ void reduce_rs_chunk(const SliceArgs &sa, int nsteps,
     }
 #pragma unroll
     for (int u = 0; u < G; ++u) store_f32_group<G, TAIL>(out, base, u, acc + 4 * u, B);
+    if (KIND) norm_total = groups_total<KIND>(norm_total, acc, base, B);
 }
 
-template <int G>
+template <int KIND, int G>
 __global__ __launch_bounds__(kThreads) void reduce_rs_chunk_kernel(SliceArgs sa, int nsteps, int world,
                                                                    int first_pass, float worldf,
-                                                                   float *__restrict__ out, int64_t n) {
+                                                                   float *__restrict__ out, int64_t n,
+                                                                   double *__restrict__ parts) {
     static_assert(G % kTailGroups == 0, "the tail walks whole sub-chunks");
-    FS_CHUNK_DISPATCH(G, (reduce_rs_chunk<G, false>(sa, nsteps, world, first_pass, worldf, out, base, n)),
-                      (reduce_rs_chunk<kTailGroups, true>(sa, nsteps, world, first_pass, worldf, out, base, n)));
+    double t = 0;
+    FS_CHUNK_DISPATCH(G, (reduce_rs_chunk<KIND, G, false>(sa, nsteps, world, first_pass, worldf, out, t, base, n)),
+                      (reduce_rs_chunk<KIND, kTailGroups, true>(sa, nsteps, world, first_pass, worldf, out, t, base,
+                                                                n)));
+    if (KIND) store_wave_total<KIND>(t, parts);
 }
 
 // Misaligned variant: 8 elements per lane, element tail.
+template <int KIND>
 __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs sa, int nsteps, int world,
                                                                      int first_pass, float worldf, int64_t n,
-                                                                     float *__restrict__ out) {
+                                                                     float *__restrict__ out,
+                                                                     double *__restrict__ parts) {
+    double total = 0;
     const int64_t nvec = n >> 3;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i < nvec) {
@@ -791,6 +839,10 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) out[8 * i + e] = acc[e];
+        if (KIND) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) total = norm_add<KIND>(total, acc[e]);
+        }
     }
     const int64_t tail = n - nvec * 8;
     if (blockIdx.x == 0 && (int64_t)threadIdx.x < tail) {
@@ -803,7 +855,9 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
             acc = (first_pass && j == 0) ? d : acc + d;
         }
         out[e] = acc;
+        if (KIND) total = norm_add<KIND>(total, acc);
     }
+    if (KIND) store_wave_total<KIND>(total, parts);
 }
 
 // ----------------------------------------------------------------- AdamW --
@@ -1234,32 +1288,56 @@ void launch_fused(int64_t n, hipStream_t stream, const SliceArgs &sa, int cnt, i
     });
 }
 
+// Call f(std::integral_constant<int, kind>) for a run-time norm kind.
+template <class F>
+void with_kind(int kind, F &&f) {
+    if (kind == kL2) f(std::integral_constant<int, kL2>{});
+    else if (kind == kInf) f(std::integral_constant<int, kInf>{});
+    else f(std::integral_constant<int, kNoNorm>{});
+}
+
+// Where a reduce leaves its partial totals: `next` moves past each launch's.
+struct NormParts {
+    int kind = kNoNorm;
+    double *next = nullptr;
+};
+
 // One pass of the fp32 reduce over terms [t0, t0 + cnt) and the sub-range
 // [off, off + len) of a call over n elements: chunked when every pointer is
 // 16-byte aligned (one launch, its last chunk partial; the residency cap is
-// decided on n), else the general kernel.
+// decided on n), else the general kernel.  The last pass leaves partial totals.
 void launch_reduce_pass(int64_t n, int64_t off, int64_t len, hipStream_t stream, const uint16_t *const *slices,
-                        int t0, int cnt, int first, int last, float world, bool aligned, float *out) {
+                        int t0, int cnt, int first, int last, float world, bool aligned, float *out,
+                        NormParts *np = nullptr) {
     SliceArgs sa;
     memset(&sa, 0, sizeof sa);
     for (int k = 0; k < cnt; ++k) sa.p[k] = slices[t0 + k] + off;
     float *o = out + off;
+    double *parts = np ? np->next : nullptr;
+    int64_t grid;
     if (aligned) {
         const bool few = cnt <= kRedFewTerms;
         const int64_t chunk = few ? kRedChunkFew : kRedChunk;
-        const dim3 g((uint32_t)((len + chunk - 1) / chunk));
+        grid = (len + chunk - 1) / chunk;
+        const dim3 g((uint32_t)grid);
         const uint32_t lds = lds_cap(few ? kRedFewWgsPerCu : kRedManyWgsPerCu, (n + chunk - 1) / chunk);
-        if (few)
-            hipLaunchKernelGGL(reduce_chunk_kernel<kRedGroupsFew>, g, dim3(kThreads), lds, stream, sa, cnt, first,
-                               last, world, o, len);
-        else
-            hipLaunchKernelGGL(reduce_chunk_kernel<kRedGroupsMany>, g, dim3(kThreads), lds, stream, sa, cnt, first,
-                               last, world, o, len);
+        with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
+            constexpr int kKind = decltype(kind)::value;
+            if (few)
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsFew>), g, dim3(kThreads), lds, stream, sa,
+                                   cnt, first, last, world, o, len, parts);
+            else
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsMany>), g, dim3(kThreads), lds, stream, sa,
+                                   cnt, first, last, world, o, len, parts);
+        });
     } else {
-        const int64_t grid = std::max<int64_t>(1, ((len >> 3) + kThreads - 1) / kThreads);
-        hipLaunchKernelGGL(reduce_general_kernel, dim3((uint32_t)grid), dim3(kThreads), 0, stream, sa, cnt, first,
-                           last, world, len, o);
+        grid = std::max<int64_t>(1, ((len >> 3) + kThreads - 1) / kThreads);
+        with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
+            hipLaunchKernelGGL((reduce_general_kernel<decltype(kind)::value>), dim3((uint32_t)grid), dim3(kThreads), 0,
+                               stream, sa, cnt, first, last, world, len, o, parts);
+        });
     }
+    if (np && last) np->next += grid * (kThreads / 64);
 }
 
 // Largest grid any launch over n elements needs: one workgroup per kAdamRow
@@ -1506,6 +1584,69 @@ int check_reduce(const char *what, int64_t n, int32_t world, int32_t grad_acc, c
     return FS_OK;
 }
 
+// The launches of a checked reduce.
+int run_reduce(const char *what, int64_t n, int32_t world, int32_t grad_acc, const uint16_t *const *slices, float *out,
+               int terms, bool aligned, hipStream_t stream, NormParts *np) {
+    for (int64_t off = 0; off < n; off += kSpan) {
+        const int64_t len = std::min(kSpan, n - off);
+        for (int t0 = 0; t0 < terms; t0 += kTermsPerPass) {
+            const int cnt = std::min(kTermsPerPass, terms - t0);
+            launch_reduce_pass(n, off, len, stream, slices, t0, cnt, t0 == 0, t0 + cnt == terms, (float)world,
+                               aligned, out, np);
+            int rc = check_launch(what);
+            if (rc != FS_OK) return rc;
+        }
+    }
+    return FS_OK;
+}
+
+// The launches of a checked reduce with the bf16 reduce dtype (world <= kTermsPerPass).
+int run_reduce_rs(const char *what, int64_t n, int32_t world, int32_t grad_acc, const uint16_t *const *slices,
+                  float *out, bool aligned, hipStream_t stream, NormParts *np) {
+    const int steps_per_pass = kTermsPerPass / world;
+    for (int64_t off = 0; off < n; off += kRsSpan) {
+        const int64_t len = std::min(kRsSpan, n - off);
+        float *o = out + off;
+        for (int j0 = 0; j0 < grad_acc; j0 += steps_per_pass) {
+            const int steps = std::min(steps_per_pass, grad_acc - j0);
+            const int first = j0 == 0;
+            const bool last = j0 + steps == grad_acc;
+            SliceArgs sa;
+            memset(&sa, 0, sizeof sa);
+            for (int k = 0; k < steps * world; ++k) sa.p[k] = slices[j0 * world + k] + off;
+            double *parts = np ? np->next : nullptr;
+            int64_t grid;
+            if (aligned) {
+                const bool few = steps * world <= kRedFewTerms;
+                const int64_t chunk = kWgRow * (few ? kRsGroupsFew : kRsGroupsMany);
+                grid = (len + chunk - 1) / chunk;
+                const dim3 g((uint32_t)grid);
+                const uint32_t lds = lds_cap(few ? kRsFewWgsPerCu : kRsManyWgsPerCu, (n + chunk - 1) / chunk);
+                with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
+                    constexpr int kKind = decltype(kind)::value;
+                    if (few)
+                        hipLaunchKernelGGL((reduce_rs_chunk_kernel<kKind, kRsGroupsFew>), g, dim3(kThreads), lds,
+                                           stream, sa, steps, (int)world, first, (float)world, o, len, parts);
+                    else
+                        hipLaunchKernelGGL((reduce_rs_chunk_kernel<kKind, kRsGroupsMany>), g, dim3(kThreads), lds,
+                                           stream, sa, steps, (int)world, first, (float)world, o, len, parts);
+                });
+            } else {
+                grid = std::max<int64_t>(1, ((len >> 3) + kThreads - 1) / kThreads);
+                with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
+                    hipLaunchKernelGGL((reduce_rs_general_kernel<decltype(kind)::value>), dim3((uint32_t)grid),
+                                       dim3(kThreads), 0, stream, sa, steps, (int)world, first, (float)world, len, o,
+                                       parts);
+                });
+            }
+            if (np && last) np->next += grid * (kThreads / 64);
+            int rc = check_launch(what);
+            if (rc != FS_OK) return rc;
+        }
+    }
+    return FS_OK;
+}
+
 }  // namespace
 
 extern "C" int fs_reduce_shard(int64_t n, int32_t world, int32_t grad_acc, const uint16_t *const *slices,
@@ -1517,17 +1658,7 @@ extern "C" int fs_reduce_shard(int64_t n, int32_t world, int32_t grad_acc, const
     if (skip) return FS_OK;
     if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "fs_reduce_shard: n too large for one launch");
     (void)hipGetLastError();
-    for (int64_t off = 0; off < n; off += kSpan) {
-        const int64_t len = std::min(kSpan, n - off);
-        for (int t0 = 0; t0 < terms; t0 += kTermsPerPass) {
-            const int cnt = std::min(kTermsPerPass, terms - t0);
-            launch_reduce_pass(n, off, len, stream, slices, t0, cnt, t0 == 0, t0 + cnt == terms, (float)world,
-                               aligned, out);
-            int rc = check_launch("fs_reduce_shard");
-            if (rc != FS_OK) return rc;
-        }
-    }
-    return FS_OK;
+    return run_reduce("fs_reduce_shard", n, world, grad_acc, slices, out, terms, aligned, stream, nullptr);
 }
 
 extern "C" int fs_reduce_shard_ex(int64_t n, int32_t world, int32_t grad_acc, fs_dtype reduce_dtype,
@@ -1542,47 +1673,24 @@ extern "C" int fs_reduce_shard_ex(int64_t n, int32_t world, int32_t grad_acc, fs
     if (skip) return FS_OK;
     if (world > kTermsPerPass)
         return fsi::fail(FS_E_UNSUPPORTED, "fs_reduce_shard_ex: bf16 reduce dtype supports world <= %d", kTermsPerPass);
-    const int steps_per_pass = kTermsPerPass / world;
     if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "fs_reduce_shard_ex: n too large for one launch");
     (void)hipGetLastError();
-    for (int64_t off = 0; off < n; off += kRsSpan) {
-        const int64_t len = std::min(kRsSpan, n - off);
-        float *o = out + off;
-        for (int j0 = 0; j0 < grad_acc; j0 += steps_per_pass) {
-            const int steps = std::min(steps_per_pass, grad_acc - j0);
-            const int first = j0 == 0;
-            SliceArgs sa;
-            memset(&sa, 0, sizeof sa);
-            for (int k = 0; k < steps * world; ++k) sa.p[k] = slices[j0 * world + k] + off;
-            if (aligned) {
-                const bool few = steps * world <= kRedFewTerms;
-                const int64_t chunk = kWgRow * (few ? kRsGroupsFew : kRsGroupsMany);
-                const dim3 g((uint32_t)((len + chunk - 1) / chunk));
-                const uint32_t lds = lds_cap(few ? kRsFewWgsPerCu : kRsManyWgsPerCu, (n + chunk - 1) / chunk);
-                if (few)
-                    hipLaunchKernelGGL(reduce_rs_chunk_kernel<kRsGroupsFew>, g, dim3(kThreads), lds, stream, sa,
-                                       steps, (int)world, first, (float)world, o, len);
-                else
-                    hipLaunchKernelGGL(reduce_rs_chunk_kernel<kRsGroupsMany>, g, dim3(kThreads), lds, stream, sa,
-                                       steps, (int)world, first, (float)world, o, len);
-            } else {
-                const int64_t grid = std::max<int64_t>(1, ((len >> 3) + kThreads - 1) / kThreads);
-                hipLaunchKernelGGL(reduce_rs_general_kernel, dim3((uint32_t)grid), dim3(kThreads), 0, stream, sa,
-                                   steps, (int)world, first, (float)world, len, o);
-            }
-            int rc = check_launch("fs_reduce_shard_ex");
-            if (rc != FS_OK) return rc;
-        }
-    }
-    return FS_OK;
+    return run_reduce_rs("fs_reduce_shard_ex", n, world, grad_acc, slices, out, aligned, stream, nullptr);
 }
 
+// Partial totals: one per wave of every workgroup of the last pass's
+// launches.  The smallest chunk is the general kernels' (kThreads * 8
+// elements); launch spans are multiples of every chunk.
 extern "C" int fs_reduce_shard_norm_workspace(int64_t n, int64_t *bytes) {
     fsi::clear_error();
     if (!bytes) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: bytes is NULL");
     if (n < 0) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: n < 0");
-    const fs_dtype f32 = FS_FP32;
-    return fs_grad_norm_workspace(1, &n, &f32, bytes);
+    constexpr int64_t kChunk = kThreads * 8;
+    static_assert(kSpan % kChunk == 0 && kRsSpan % kChunk == 0 && kRedChunkFew >= kChunk && kWgRow * kRsGroupsFew >= kChunk,
+                  "the workspace counts chunks of kChunk elements");
+    const int64_t waves = (n / kChunk + (n % kChunk != 0)) * (kThreads / 64);
+    *bytes = norm_parts_bytes(waves);
+    return FS_OK;
 }
 
 extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, fs_dtype reduce_dtype,
@@ -1596,11 +1704,12 @@ extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, 
     if (reduce_dtype != FS_BF16 && reduce_dtype != FS_FP32) return fsi::fail(FS_E_DTYPE, "%s: unknown reduce dtype", what);
     if (reduce_dtype == FS_BF16 && world > kTermsPerPass)
         return fsi::fail(FS_E_UNSUPPORTED, "%s: bf16 reduce dtype supports world <= %d", what, kTermsPerPass);
+    if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "%s: n too large for one launch", what);
     if (int rc = check_norm_out(what, type, total, norm)) return rc;
     int64_t need = 0;
     if (int rc = fs_reduce_shard_norm_workspace(n, &need)) return rc;
     if (int rc = check_workspace_range(what, workspace, bytes, need, total, norm)) return rc;
-    if (n > 0) {
+    if (!skip) {
         const void *arr[3] = {total, norm, workspace};
         const int64_t len[3] = {8, norm ? 4 : 0, need};
         static const char *const name[3] = {"total", "norm", "workspace"};
@@ -1610,12 +1719,17 @@ extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, 
                 if (ranges_overlap(arr[i], len[i], slices[t], 2 * n))
                     return fsi::fail(FS_E_INVAL, "%s: %s overlaps slice %d", what, name[i], t);
         }
-        if (!grid_fits(n)) return fsi::fail(FS_E_OVERFLOW, "%s: n too large for one launch", what);
     }
-    if (int rc = fs_reduce_shard_ex(n, world, grad_acc, reduce_dtype, slices, out, stream)) return rc;
-    const fs_dtype f32 = FS_FP32;
-    const void *grads = out;
-    return fs_grad_norm(1, &grads, &n, &f32, type, accumulate, total, norm, workspace, bytes, stream);
+    (void)hipGetLastError();
+    double *parts = static_cast<double *>(workspace);
+    NormParts np{(int)type, parts};
+    if (!skip) {
+        const int rc = reduce_dtype == FS_FP32
+                           ? run_reduce(what, n, world, grad_acc, slices, out, terms, aligned, stream, &np)
+                           : run_reduce_rs(what, n, world, grad_acc, slices, out, aligned, stream, &np);
+        if (rc != FS_OK) return rc;
+    }
+    return launch_norm_finish(what, type, accumulate != 0, parts, np.next - parts, total, norm, stream);
 }
 
 extern "C" int fs_pack_cast(fs_plan_t plan, const void *const *params, fs_dtype param_dtype, void *out,

@@ -34,12 +34,19 @@ __device__ __forceinline__ double norm_add(double t, float x) {
     return norm_join<KIND>(t, (double)fabsf(x));
 }
 
-// The workgroup's total, in thread 0 (the other threads get parts of it).
-// `lds`: one double per wave.  A fixed tree: the same for every launch.
-template <int KIND, int THREADS>
-__device__ __forceinline__ double norm_block_join(double t, double *lds) {
+// The wave's total, in lane 0.  A fixed tree: the same for every launch.
+template <int KIND>
+__device__ __forceinline__ double norm_wave_join(double t) {
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) t = norm_join<KIND>(t, __shfl_down(t, d));
+    return t;
+}
+
+// The workgroup's total, in thread 0 (the other threads get parts of it).
+// `lds`: one double per wave.
+template <int KIND, int THREADS>
+__device__ __forceinline__ double norm_block_join(double t, double *lds) {
+    t = norm_wave_join<KIND>(t);
     if constexpr (THREADS > 64) {
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = t;
         __syncthreads();
@@ -72,7 +79,10 @@ int check_norm_out(const char *what, int type, const double *total, const float 
 int check_clip(const char *what, const fs_clip_t *clip, ClipArgs *out);
 int check_workspace_range(const char *what, const void *workspace, size_t bytes, int64_t need, const double *total,
                           const float *norm);
-int launch_norm_finish(const char *what, int type, int accumulate, const double *parts, int64_t count, double *total,
+// Workspace bytes for `count` partial totals: what launch_norm_finish needs.
+int64_t norm_parts_bytes(int64_t count);
+// Joins the partial totals into total and norm; parts has norm_parts_bytes(count) bytes.
+int launch_norm_finish(const char *what, int type, int accumulate, double *parts, int64_t count, double *total,
                        float *norm, hipStream_t stream);
 
 }  // namespace fsi

@@ -127,6 +127,22 @@ __global__ __launch_bounds__(kThreads) void list_norm_kernel(ListArgs L, int cou
     if (threadIdx.x == 0) parts[blockIdx.x] = t;
 }
 
+// Many partial totals are first joined to kJoinWgs, each workgroup's in a
+// contiguous piece; one workgroup would read them at one CU's rate.
+constexpr int kJoinWgs = 512;
+constexpr int64_t kJoinMin = 8192;
+
+template <int KIND>
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(const double *__restrict__ parts, int64_t count,
+                                                             double *__restrict__ out) {
+    __shared__ double lds[kThreads / 64];
+    const int64_t lo = count * blockIdx.x / kJoinWgs, hi = count * (blockIdx.x + 1) / kJoinWgs;
+    double t = 0;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) t = norm_join<KIND>(t, parts[i]);
+    t = norm_block_join<KIND, kThreads>(t, lds);
+    if (threadIdx.x == 0) out[blockIdx.x] = t;
+}
+
 // Joins the partial totals in a fixed order; writes the total (joined to the
 // one that stands there, where the call accumulates) and the norm.
 constexpr int kFinishThreads = 1024;
@@ -305,8 +321,21 @@ int check_workspace_range(const char *what, const void *workspace, size_t bytes,
     return FS_OK;
 }
 
-int launch_norm_finish(const char *what, int type, int accumulate, const double *parts, int64_t count, double *total,
+int64_t norm_parts_bytes(int64_t count) {
+    return (count + (count > kJoinMin ? kJoinWgs : 0)) * (int64_t)sizeof(double);
+}
+
+int launch_norm_finish(const char *what, int type, int accumulate, double *parts, int64_t count, double *total,
                        float *norm, hipStream_t stream) {
+    if (count > kJoinMin) {
+        double *joined = parts + count;
+        if (type == FS_NORM_L2)
+            hipLaunchKernelGGL(norm_join_kernel<kL2>, dim3(kJoinWgs), dim3(kThreads), 0, stream, parts, count, joined);
+        else
+            hipLaunchKernelGGL(norm_join_kernel<kInf>, dim3(kJoinWgs), dim3(kThreads), 0, stream, parts, count, joined);
+        parts = joined;
+        count = kJoinWgs;
+    }
     if (type == FS_NORM_L2)
         hipLaunchKernelGGL(norm_finish_kernel<kL2>, dim3(1), dim3(kFinishThreads), 0, stream, parts, count, accumulate,
                            total, norm);
@@ -324,7 +353,7 @@ extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, c
     if (!bytes) return fail(FS_E_INVAL, "fs_grad_norm_workspace: bytes is NULL");
     if (n_tensors < 0) return fail(FS_E_INVAL, "fs_grad_norm_workspace: n_tensors < 0");
     if (n_tensors > 0 && (!numel || !dtypes)) return fail(FS_E_INVAL, "fs_grad_norm_workspace: NULL list");
-    *bytes = ((int64_t)n_tensors + kListMax - 1) / kListMax * kNormWgs * (int64_t)sizeof(double);
+    *bytes = norm_parts_bytes(((int64_t)n_tensors + kListMax - 1) / kListMax * kNormWgs);
     return FS_OK;
 }
 
