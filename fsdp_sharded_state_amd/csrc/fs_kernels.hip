@@ -485,13 +485,13 @@ __device__ __forceinline__ u32x4 ld_slice16(const uint16_t *p, int64_t off) {
     return funnel16(lo, hi, sh);
 }
 
-// Lane 0 writes its wave's partial total.  One per wave, with no barrier: at
+// Each wave writes its partial total.  One per wave, with no barrier: at
 // one to three workgroups per CU the waves of a workgroup should not wait for
 // each other.
 template <int KIND>
-__device__ __forceinline__ void store_wave_total(double t, double *__restrict__ parts) {
-    t = norm_wave_join<KIND>(t);
-    if ((threadIdx.x & 63) == 0) parts[(int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = t;
+__device__ __forceinline__ void store_wave_total(const LaneTotal<KIND> &t, double *__restrict__ parts) {
+    const double sum = norm_wave_join<KIND>(t.value());
+    if ((threadIdx.x & 63) == 63) parts[(int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = sum;
 }
 
 // Misaligned slices or output: lane i owns 8 consecutive elements, one
@@ -502,7 +502,7 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
                                                                   int last_pass, float world, int64_t n,
                                                                   float *__restrict__ out,
                                                                   double *__restrict__ parts) {
-    double total = 0;
+    LaneTotal<KIND> total;
     const int64_t nvec = n >> 3;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i < nvec) {
@@ -532,7 +532,7 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
         for (int e = 0; e < 8; ++e) out[8 * i + e] = acc[e];
         if (KIND) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) total = norm_add<KIND>(total, acc[e]);
+            for (int e = 0; e < 8; ++e) total.add(acc[e]);
         }
     }
     const int64_t tail = n - nvec * 8;
@@ -549,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
         for (; t < nterms; ++t) acc = acc + __uint_as_float((uint32_t)sa.p[t][e] << 16);
         if (last_pass) acc = acc / world;
         out[e] = acc;
-        if (KIND) total = norm_add<KIND>(total, acc);
+        if (KIND) total.add(acc);
     }
     if (KIND) store_wave_total<KIND>(total, parts);
 }
@@ -642,14 +642,14 @@ __device__ __forceinline__ void store_f32_group(float *p, int64_t base, int u, c
 
 // The total of the lane's G groups (the elements below n), added to t.
 template <int KIND, int G, bool TAIL>
-__device__ __forceinline__ double groups_total(double t, const float *v, int64_t base, const Bounds<G, TAIL> &B) {
+__device__ __forceinline__ void add_groups(LaneTotal<KIND> &t, const float *v, int64_t base,
+                                           const Bounds<G, TAIL> &B) {
 #pragma unroll
     for (int u = 0; u < G; ++u) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (!TAIL || base + u * kWgRow + k < B.n) t = norm_add<KIND>(t, v[4 * u + k]);
+            if (!TAIL || base + u * kWgRow + k < B.n) t.add(v[4 * u + k]);
     }
-    return t;
 }
 
 // Sum the lane's G groups over slices 0..nterms-1 in slice order, into acc
@@ -684,7 +684,7 @@ __device__ __forceinline__ void sum_slices(const SliceArgs &sa, int nterms, bool
 
 template <int KIND, int G, bool TAIL>
 __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, int first_pass, int last_pass,
-                                             float world, float *__restrict__ out, double &norm_total,
+                                             float world, float *__restrict__ out, LaneTotal<KIND> &lane_total,
                                              int64_t base, int64_t n) {
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G];
@@ -696,7 +696,7 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
     }
 #pragma unroll
     for (int u = 0; u < G; ++u) store_f32_group<G, TAIL>(out, base, u, acc + 4 * u, B);
-    if (KIND) norm_total = groups_total<KIND>(norm_total, acc, base, B);
+    if (KIND) add_groups<KIND>(lane_total, acc, base, B);
 }
 
 // The chunk of workgroup blockIdx.x: whole, or the last one cut by n (walked
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, in
                                                                 float *__restrict__ out, int64_t n,
                                                                 double *__restrict__ parts) {
     static_assert(G % kTailGroups == 0, "the tail walks whole sub-chunks");
-    double t = 0;
+    LaneTotal<KIND> t;
     FS_CHUNK_DISPATCH(G, (reduce_chunk<KIND, G, false>(sa, nterms, first_pass, last_pass, world, out, t, base, n)),
                       (reduce_chunk<KIND, kTailGroups, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
                                                              n)));
@@ -751,7 +751,7 @@ __device__ __forceinline__ float bf16_round_f32(float f) {
 
 template <int KIND, int G, bool TAIL>
 __device__ __forceinline__ void reduce_rs_chunk(const SliceArgs &sa, int nsteps, int world, int first_pass,
-                                                float worldf, float *__restrict__ out, double &norm_total,
+                                                float worldf, float *__restrict__ out, LaneTotal<KIND> &lane_total,
                                                 int64_t base, int64_t n) {
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G], sum[4 * G];
@@ -796,7 +796,7 @@ __device__ __forceinline__ void reduce_rs_chunk(const SliceArgs &sa, int nsteps,
     }
 #pragma unroll
     for (int u = 0; u < G; ++u) store_f32_group<G, TAIL>(out, base, u, acc + 4 * u, B);
-    if (KIND) norm_total = groups_total<KIND>(norm_total, acc, base, B);
+    if (KIND) add_groups<KIND>(lane_total, acc, base, B);
 }
 
 template <int KIND, int G>
@@ -805,7 +805,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_chunk_kernel(SliceArgs sa,
                                                                    float *__restrict__ out, int64_t n,
                                                                    double *__restrict__ parts) {
     static_assert(G % kTailGroups == 0, "the tail walks whole sub-chunks");
-    double t = 0;
+    LaneTotal<KIND> t;
     FS_CHUNK_DISPATCH(G, (reduce_rs_chunk<KIND, G, false>(sa, nsteps, world, first_pass, worldf, out, t, base, n)),
                       (reduce_rs_chunk<KIND, kTailGroups, true>(sa, nsteps, world, first_pass, worldf, out, t, base,
                                                                 n)));
@@ -818,7 +818,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
                                                                      int first_pass, float worldf, int64_t n,
                                                                      float *__restrict__ out,
                                                                      double *__restrict__ parts) {
-    double total = 0;
+    LaneTotal<KIND> total;
     const int64_t nvec = n >> 3;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i < nvec) {
@@ -841,7 +841,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
         for (int e = 0; e < 8; ++e) out[8 * i + e] = acc[e];
         if (KIND) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) total = norm_add<KIND>(total, acc[e]);
+            for (int e = 0; e < 8; ++e) total.add(acc[e]);
         }
     }
     const int64_t tail = n - nvec * 8;
@@ -855,7 +855,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
             acc = (first_pass && j == 0) ? d : acc + d;
         }
         out[e] = acc;
-        if (KIND) total = norm_add<KIND>(total, acc);
+        if (KIND) total.add(acc);
     }
     if (KIND) store_wave_total<KIND>(total, parts);
 }

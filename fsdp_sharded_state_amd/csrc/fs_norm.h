@@ -23,22 +23,48 @@ __device__ __forceinline__ double norm_join(double a, double b) {
     return a != a || a > b ? a : b;   // b if it is NaN: a > NaN is false
 }
 
-// One value's share of the total, added to t.  The square is exact (48
-// significant bits), so the fused multiply-add rounds only the sum.
+// A lane's running total.  L2: a double; the square of an fp32 value is exact
+// in it (48 significant bits), so the fused multiply-add rounds only the sum.
+// INF: the largest magnitude as fp32 bits, whose order as integers is that of
+// the magnitudes, with the infinity above every number and NaN above it (two
+// integer instructions a value; comparing doubles made the reduce 3% slower).
 template <int KIND>
-__device__ __forceinline__ double norm_add(double t, float x) {
-    if (KIND == kL2) {
+struct LaneTotal {
+    double t = 0;
+    __device__ __forceinline__ void add(float x) {
         const double d = x;
-        return fma(d, d, t);
+        t = fma(d, d, t);
     }
-    return norm_join<KIND>(t, (double)fabsf(x));
+    __device__ __forceinline__ double value() const { return t; }
+};
+template <>
+struct LaneTotal<kInf> {
+    uint32_t m = 0;
+    __device__ __forceinline__ void add(float x) { m = max(m, __float_as_uint(x) & 0x7FFFFFFFu); }
+    __device__ __forceinline__ double value() const { return (double)__uint_as_float(m); }
+};
+
+// A double from the lanes CTRL names (data parallel primitives: no LDS, a few
+// cycles); zero, which adds nothing to either total, where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double x) {
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
 }
 
-// The wave's total, in lane 0.  A fixed tree: the same for every launch.
+// The wave's total, in lane 63.  A fixed tree: the same for every launch.
+// Shifts by 1, 2, 4 and 8 lanes sum up each row of 16, the broadcasts of
+// lanes 15 and 31 carry the rows' sums on.
 template <int KIND>
 __device__ __forceinline__ double norm_wave_join(double t) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) t = norm_join<KIND>(t, __shfl_down(t, d));
+    t = norm_join<KIND>(t, dpp_or_zero<0x111, 0xF>(t));   // row_shr:1
+    t = norm_join<KIND>(t, dpp_or_zero<0x112, 0xF>(t));   // row_shr:2
+    t = norm_join<KIND>(t, dpp_or_zero<0x114, 0xF>(t));   // row_shr:4
+    t = norm_join<KIND>(t, dpp_or_zero<0x118, 0xF>(t));   // row_shr:8
+    t = norm_join<KIND>(t, dpp_or_zero<0x142, 0xA>(t));   // row_bcast:15 into rows 1 and 3
+    t = norm_join<KIND>(t, dpp_or_zero<0x143, 0xC>(t));   // row_bcast:31 into rows 2 and 3
     return t;
 }
 
@@ -47,11 +73,12 @@ __device__ __forceinline__ double norm_wave_join(double t) {
 template <int KIND, int THREADS>
 __device__ __forceinline__ double norm_block_join(double t, double *lds) {
     t = norm_wave_join<KIND>(t);
-    if constexpr (THREADS > 64) {
-        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = t;
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int w = 1; w < THREADS / 64; ++w) t = norm_join<KIND>(t, lds[w]);
+    if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        t = lds[0];
+#pragma unroll
+        for (int w = 1; w < THREADS / 64; ++w) t = norm_join<KIND>(t, lds[w]);
     }
     return t;
 }

@@ -80,22 +80,21 @@ __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w <<
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 template <int KIND, int W>
-__device__ __forceinline__ double block_total(double t, u32x4 v) {
+__device__ __forceinline__ void add_block(LaneTotal<KIND> &t, u32x4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if (W == 4) {
-            t = norm_add<KIND>(t, __uint_as_float(w[i]));
+            t.add(__uint_as_float(w[i]));
         } else {
-            t = norm_add<KIND>(t, bf_lo(w[i]));
-            t = norm_add<KIND>(t, bf_hi(w[i]));
+            t.add(bf_lo(w[i]));
+            t.add(bf_hi(w[i]));
         }
     }
-    return t;
 }
 
 template <int KIND, int W>
-__device__ __forceinline__ double tile_total(double t, const TileAt &at) {
+__device__ __forceinline__ void add_tile(LaneTotal<KIND> &t, const TileAt &at) {
     u32x4 v[kNormUnroll];
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) {
@@ -111,20 +110,19 @@ __device__ __forceinline__ double tile_total(double t, const TileAt &at) {
         }
     }
 #pragma unroll
-    for (int u = 0; u < kNormUnroll; ++u) t = block_total<KIND, W>(t, v[u]);
-    return t;
+    for (int u = 0; u < kNormUnroll; ++u) add_block<KIND, W>(t, v[u]);
 }
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void list_norm_kernel(ListArgs L, int count, uint32_t ntiles, double *parts) {
     __shared__ double lds[kThreads / 64];
-    double t = 0;
+    LaneTotal<KIND> t;
     for (uint32_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
         const TileAt at = tile_at<kNormTile>(L, count, tile);
-        t = at.f32 ? tile_total<KIND, 4>(t, at) : tile_total<KIND, 2>(t, at);
+        if (at.f32) add_tile<KIND, 4>(t, at); else add_tile<KIND, 2>(t, at);
     }
-    t = norm_block_join<KIND, kThreads>(t, lds);
-    if (threadIdx.x == 0) parts[blockIdx.x] = t;
+    const double sum = norm_block_join<KIND, kThreads>(t.value(), lds);
+    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
 // Many partial totals are first joined to kJoinWgs, each workgroup's in a
