@@ -559,13 +559,14 @@ def fs_reduce_adamw_step_noalloc(slices: Sequence[torch.Tensor], master: torch.T
                                               ptr(param_bf16, "param_bf16"), ctypes.byref(hp), _stream(stream)))
 
 
+_NORM_CODES = {2: FS_NORM_L2, "2": FS_NORM_L2, math.inf: FS_NORM_INF, "inf": FS_NORM_INF}
+
+
 def _norm_code(norm_type) -> int:
-    p = float(norm_type)
-    if p == 2.0:
-        return FS_NORM_L2
-    if p == math.inf:
-        return FS_NORM_INF
-    raise ValueError(f"unsupported norm_type {norm_type!r}: 2 and inf are defined")
+    code = _NORM_CODES.get(norm_type)
+    if code is None:
+        raise ValueError(f"unsupported norm_type {norm_type!r}: 2 and inf are defined")
+    return code
 
 
 class GradList:
@@ -578,19 +579,20 @@ class GradList:
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         n = len(tensors)
-        ptrs, numels, codes, device, storages = [], [], [], None, {}
+        ptrs, numels, codes, index, storages = [], [], [], None, {}
         for i, t in enumerate(tensors):
             ptrs.append(_dev_ptr(t, f"tensor {i}"))
             numels.append(t.numel())
             codes.append(_dtype_code(t.dtype))
-            if device is None:
-                device = t.device
-            elif t.device != device:
-                raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {device}")
+            if index is None:
+                index = t.get_device()
+            elif t.get_device() != index:
+                raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {tensors[0].device}")
             st = t.untyped_storage()
             storages[st.data_ptr()] = (st, st.data_ptr(), st.nbytes())
-        self.device: Optional[torch.device] = device
+        self._index: Optional[int] = index          # of their GPU; None for an empty list
         self.numels, self.codes = numels, codes
+        self._same = (codes[0], numels[0]) if n and len(set(codes)) == 1 and len(set(numels)) == 1 else None
         self._storages = list(storages.values())
         self._tensors = [t.detach() for t in tensors]   # aliases: they keep the memory
         self._n = n
@@ -621,31 +623,39 @@ def _grad_list(tensors) -> GradList:
     return tensors._live() if isinstance(tensors, GradList) else GradList(tensors)
 
 
-def _scalar_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, device, what: str) -> Optional[int]:
+def _scalar_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, index: Optional[int], what: str) -> Optional[int]:
+    """Address of a one-value tensor on GPU `index` (None: on any GPU)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != 1:
+    if t.dtype is not dtype or t.numel() != 1:
         raise ValueError(f"{what} must be one {dtype} value")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the gradients on {device}")
-    return _dev_ptr(t, what)
+    if t.get_device() != index:
+        if index is not None and index >= 0:
+            raise ValueError(f"{what} is on {t.device}, the gradients on cuda:{index}")
+        if not t.is_cuda:
+            raise ValueError(f"{what} must be a GPU tensor")
+    return t.data_ptr()
 
 
-def _launch(device: torch.device, stream, fn, *args, scratch: int = -1):
-    """Run a launching call with `device` current, on `stream` (default: that
-    device's current stream).  scratch >= 0: that many workspace bytes and
+def _launch(index: int, stream, fn, *args, scratch: int = -1):
+    """Run a launching call with GPU `index` current, on `stream` (default:
+    that GPU's current stream).  scratch >= 0: that many workspace bytes and
     their count go before the stream; they belong to the stream the kernels
     run on, so the allocator hands them out again in that stream's order."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(device, stream, fn, *args, scratch=scratch)
-    handle = _stream(stream)
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _launch(index, stream, fn, *args, scratch=scratch)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = _stream(stream)
+        if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     if scratch < 0:
         return _check(fn(*args, handle))
     if scratch == 0:
         return _check(fn(*args, None, 0, handle))
+    device = torch.device("cuda", index)
     if stream is None:
         ws = torch.empty(scratch, dtype=torch.uint8, device=device)
     else:
@@ -664,10 +674,10 @@ def fs_grad_norm(grads, total: torch.Tensor, norm: Optional[torch.Tensor] = None
     to the total that stands there."""
     kind = _norm_code(norm_type)
     gl = _grad_list(grads)
-    tot = _scalar_ptr(total, torch.float64, gl.device, "total")
-    nrm = _scalar_ptr(norm, torch.float32, total.device, "norm")
-    _launch(total.device, stream, lib().fs_grad_norm, gl._n, gl._ptrs, gl._numels, gl._codes, kind, int(accumulate),
-            tot, nrm, scratch=gl._norm_bytes)
+    tot = _scalar_ptr(total, torch.float64, gl._index, "total")
+    index = total.get_device()
+    _launch(index, stream, lib().fs_grad_norm, gl._n, gl._ptrs, gl._numels, gl._codes, kind, int(accumulate),
+            tot, _scalar_ptr(norm, torch.float32, index, "norm"), scratch=gl._norm_bytes)
 
 
 def fs_clip_grads(grads, total: torch.Tensor, max_norm: float, norm: Optional[torch.Tensor] = None, *, norm_type=2.0,
@@ -676,9 +686,10 @@ def fs_clip_grads(grads, total: torch.Tensor, max_norm: float, norm: Optional[to
     + norm_eps)); norm (float32, one value) receives the norm of the total."""
     kind = _norm_code(norm_type)
     gl = _grad_list(grads)
-    clip = Clip(_scalar_ptr(total, torch.float64, gl.device, "total"), max_norm, norm_eps, kind)
-    nrm = _scalar_ptr(norm, torch.float32, total.device, "norm")
-    _launch(total.device, stream, lib().fs_clip_grads, gl._n, gl._ptrs, gl._numels, gl._codes, ctypes.byref(clip), nrm)
+    clip = Clip(_scalar_ptr(total, torch.float64, gl._index, "total"), max_norm, norm_eps, kind)
+    index = total.get_device()
+    _launch(index, stream, lib().fs_clip_grads, gl._n, gl._ptrs, gl._numels, gl._codes, ctypes.byref(clip),
+            _scalar_ptr(norm, torch.float32, index, "norm"))
 
 
 def fs_reduce_shard_norm(slices, out: torch.Tensor, total: torch.Tensor, norm: Optional[torch.Tensor] = None, *,
@@ -688,21 +699,22 @@ def fs_reduce_shard_norm(slices, out: torch.Tensor, total: torch.Tensor, norm: O
     norm of the averaged gradients, as fs_grad_norm gives them for out."""
     kind = _norm_code(norm_type)
     n = out.numel()
-    if out.dtype != torch.float32:
+    if out.dtype is not torch.float32:
         raise ValueError("fs_reduce_shard_norm: out must be float32")
     if len(slices) != world * grad_acc:
         raise ValueError(f"fs_reduce_shard_norm: need world*grad_acc = {world * grad_acc} slices")
     gl = _grad_list(slices)
-    if gl._n and gl.device != out.device:
-        raise ValueError(f"fs_reduce_shard_norm: out is on {out.device}, the slices on {gl.device}")
-    if any(c != FS_BF16 for c in gl.codes) or any(m != n for m in gl.numels):
+    if gl._n and gl._same != (FS_BF16, n):
         raise ValueError(f"fs_reduce_shard_norm: every slice must be bf16 with {n} elements")
+    index = out.get_device()
+    if gl._n and gl._index != index:
+        raise ValueError(f"fs_reduce_shard_norm: out is on {out.device}, the slices on cuda:{gl._index}")
+    ptr = _dev_ptr(out, "out")
     need = ctypes.c_int64()
     _check(lib().fs_reduce_shard_norm_workspace(n, ctypes.byref(need)))
-    _launch(out.device, stream, lib().fs_reduce_shard_norm, n, int(world), int(grad_acc), _dtype_code(reduce_dtype),
-            gl._ptrs, _dev_ptr(out, "out") if n else 0, kind, int(accumulate),
-            _scalar_ptr(total, torch.float64, out.device, "total"),
-            _scalar_ptr(norm, torch.float32, out.device, "norm"), scratch=need.value)
+    _launch(index, stream, lib().fs_reduce_shard_norm, n, int(world), int(grad_acc), _dtype_code(reduce_dtype),
+            gl._ptrs, ptr if n else 0, kind, int(accumulate), _scalar_ptr(total, torch.float64, index, "total"),
+            _scalar_ptr(norm, torch.float32, index, "norm"), scratch=need.value)
 
 
 def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, grad: torch.Tensor,
@@ -713,24 +725,24 @@ def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: 
     """fs_adamw_step on the gradient times min(1, max_norm / (norm_of(total) +
     norm_eps)), applied as the gradient is read."""
     kind = _norm_code(norm_type)
-    n = master.numel()
-    for name, t in (("master", master), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq)):
-        if t.dtype != torch.float32 or t.numel() != n:
-            raise ValueError(f"fs_adamw_step_clip: {name} must be float32 with {n} elements")
-    if grad.numel() != n or grad.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("fs_adamw_step_clip: grad must be float32 or bfloat16 with n elements")
-    if param_bf16 is not None and (param_bf16.dtype != torch.bfloat16 or param_bf16.numel() != n):
-        raise ValueError("fs_adamw_step_clip: param_bf16 must be bfloat16 with n elements")
-    dev = master.device
-    for name, t in (("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq), ("grad", grad), ("param_bf16", param_bf16)):
-        if t is not None and t.device != dev:
-            raise ValueError(f"fs_adamw_step_clip: {name} is on {t.device}, master on {dev}")
+    n, index = master.numel(), master.get_device()
+    f32, bf16 = torch.float32, torch.bfloat16
+    arrays = [("master", master, (f32,)), ("exp_avg", exp_avg, (f32,)), ("exp_avg_sq", exp_avg_sq, (f32,)),
+              ("grad", grad, (f32, bf16))]
+    if param_bf16 is not None:
+        arrays.append(("param_bf16", param_bf16, (bf16,)))
+    for name, t, dtypes in arrays:
+        if t.dtype not in dtypes or t.numel() != n:
+            raise ValueError(f"fs_adamw_step_clip: {name} must be {' or '.join(map(str, dtypes))} with {n} elements")
+        if t.get_device() != index:
+            raise ValueError(f"fs_adamw_step_clip: {name} is on {t.device}, master on {master.device}")
+    clip = Clip(_scalar_ptr(total, torch.float64, index, "total"), max_norm, norm_eps, kind)
+    ptrs = [_dev_ptr(t, name) if n else 0 for name, t, _ in arrays]
+    th, m, v, g = ptrs[:4]
+    p16 = ptrs[4] if param_bf16 is not None else None
     hp = AdamWHparams(lr, beta1, beta2, eps, weight_decay, 0, int(step))
-    clip = Clip(_scalar_ptr(total, torch.float64, dev, "total"), max_norm, norm_eps, kind)
-    ptr = (lambda t, w: _dev_ptr(t, w) if n else 0)
-    _launch(dev, stream, lib().fs_adamw_step_clip, n, ptr(master, "master"), ptr(exp_avg, "exp_avg"),
-            ptr(exp_avg_sq, "exp_avg_sq"), ptr(grad, "grad"), FS_BF16 if grad.dtype == torch.bfloat16 else FS_FP32,
-            ptr(param_bf16, "param_bf16") if param_bf16 is not None else None, ctypes.byref(hp), ctypes.byref(clip))
+    _launch(index, stream, lib().fs_adamw_step_clip, n, th, m, v, g,
+            FS_BF16 if grad.dtype is bf16 else FS_FP32, p16, ctypes.byref(hp), ctypes.byref(clip))
 
 
 def fs_copy_bytes(dst: torch.Tensor, src: torch.Tensor, stream=None):

@@ -490,7 +490,7 @@ __device__ __forceinline__ u32x4 ld_slice16(const uint16_t *p, int64_t off) {
 // each other.
 template <int KIND>
 __device__ __forceinline__ void store_wave_total(const LaneTotal<KIND> &t, double *__restrict__ parts) {
-    const double sum = norm_wave_join<KIND>(t.value());
+    const double sum = norm_wave_join<KIND>(t);
     if ((threadIdx.x & 63) == 63) parts[(int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = sum;
 }
 

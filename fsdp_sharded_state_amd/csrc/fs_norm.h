@@ -35,44 +35,56 @@ struct LaneTotal {
         const double d = x;
         t = fma(d, d, t);
     }
-    __device__ __forceinline__ double value() const { return t; }
 };
 template <>
 struct LaneTotal<kInf> {
     uint32_t m = 0;
     __device__ __forceinline__ void add(float x) { m = max(m, __float_as_uint(x) & 0x7FFFFFFFu); }
-    __device__ __forceinline__ double value() const { return (double)__uint_as_float(m); }
 };
 
-// A double from the lanes CTRL names (data parallel primitives: no LDS, a few
-// cycles); zero, which adds nothing to either total, where there is none.
+// The value that the lanes CTRL names hold (data parallel primitives: no LDS,
+// a few cycles); zero, which adds nothing to either total, where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp_or_zero(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, true);
+}
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_or_zero(double x) {
     const uint64_t b = (uint64_t)__double_as_longlong(x);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
-    return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+    const uint64_t hi = dpp_or_zero<CTRL, ROWS>((uint32_t)(b >> 32));
+    return __longlong_as_double((long long)((hi << 32) | dpp_or_zero<CTRL, ROWS>((uint32_t)b)));
 }
 
-// The wave's total, in lane 63.  A fixed tree: the same for every launch.
-// Shifts by 1, 2, 4 and 8 lanes sum up each row of 16, the broadcasts of
-// lanes 15 and 31 carry the rows' sums on.
+// x joined over the wave, in lane 63.  A fixed tree: the same for every
+// launch.  Shifts by 1, 2, 4 and 8 lanes join each row of 16, the broadcasts
+// of lanes 15 and 31 carry the rows' results on.
+template <class T, class F>
+__device__ __forceinline__ T wave_join(T x, F &&join) {
+    x = join(x, dpp_or_zero<0x111, 0xF>(x));   // row_shr:1
+    x = join(x, dpp_or_zero<0x112, 0xF>(x));   // row_shr:2
+    x = join(x, dpp_or_zero<0x114, 0xF>(x));   // row_shr:4
+    x = join(x, dpp_or_zero<0x118, 0xF>(x));   // row_shr:8
+    x = join(x, dpp_or_zero<0x142, 0xA>(x));   // row_bcast:15 into rows 1 and 3
+    x = join(x, dpp_or_zero<0x143, 0xC>(x));   // row_bcast:31 into rows 2 and 3
+    return x;
+}
 template <int KIND>
 __device__ __forceinline__ double norm_wave_join(double t) {
-    t = norm_join<KIND>(t, dpp_or_zero<0x111, 0xF>(t));   // row_shr:1
-    t = norm_join<KIND>(t, dpp_or_zero<0x112, 0xF>(t));   // row_shr:2
-    t = norm_join<KIND>(t, dpp_or_zero<0x114, 0xF>(t));   // row_shr:4
-    t = norm_join<KIND>(t, dpp_or_zero<0x118, 0xF>(t));   // row_shr:8
-    t = norm_join<KIND>(t, dpp_or_zero<0x142, 0xA>(t));   // row_bcast:15 into rows 1 and 3
-    t = norm_join<KIND>(t, dpp_or_zero<0x143, 0xC>(t));   // row_bcast:31 into rows 2 and 3
-    return t;
+    return wave_join(t, [](double a, double b) { return norm_join<KIND>(a, b); });
+}
+template <int KIND>
+__device__ __forceinline__ double norm_wave_join(const LaneTotal<KIND> &t) {
+    if constexpr (KIND == kInf)
+        return (double)__uint_as_float(wave_join(t.m, [](uint32_t a, uint32_t b) { return max(a, b); }));
+    else
+        return norm_wave_join<KIND>(t.t);
 }
 
 // The workgroup's total, in thread 0 (the other threads get parts of it).
 // `lds`: one double per wave.
-template <int KIND, int THREADS>
-__device__ __forceinline__ double norm_block_join(double t, double *lds) {
-    t = norm_wave_join<KIND>(t);
+template <int KIND, int THREADS, class T>
+__device__ __forceinline__ double norm_block_join(const T &lane, double *lds) {
+    double t = norm_wave_join<KIND>(lane);
     if ((threadIdx.x & 63) == 63) lds[threadIdx.x >> 6] = t;
     __syncthreads();
     if (threadIdx.x == 0) {

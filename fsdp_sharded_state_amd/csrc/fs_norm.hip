@@ -25,11 +25,13 @@ using namespace fsi;
 namespace {
 
 constexpr int kListMax = 192;   // tensors of one launch: the list takes 3840 of the 4096 argument bytes
+constexpr int kListFew = 16;    // shorter lists take 320
 
+template <int CAP>
 struct ListArgs {
-    char *ptr[kListMax];            // first element
-    int64_t size[kListMax];         // bytes * 2, + 1 for fp32
-    uint32_t tile_end[kListMax];    // tiles of this tensor and those before it
+    char *ptr[CAP];            // first element
+    int64_t size[CAP];         // bytes * 2, + 1 for fp32
+    uint32_t tile_end[CAP];    // tiles of this tensor and those before it; UINT32_MAX past the last tensor
 };
 
 // A tile's place: blocks [first, first + nblk) of the tensor whose bytes are
@@ -41,13 +43,9 @@ struct TileAt {
     bool f32, whole;   // whole: no element of any of the blocks lies outside the tensor
 };
 
-template <int TILE>
-__device__ __forceinline__ TileAt tile_at(const ListArgs &L, int count, uint32_t tile) {
-    int a = 0, b = count - 1;   // the first tensor whose tile_end lies above `tile`
-    while (a < b) {
-        const int mid = (a + b) >> 1;
-        if (L.tile_end[mid] <= tile) a = mid + 1; else b = mid;
-    }
+// The place of tile `tile` (of `blocks` blocks), which is one of tensor a's.
+template <int CAP>
+__device__ __forceinline__ TileAt tile_of(const ListArgs<CAP> &L, int a, uint32_t tile, int blocks) {
     const uint32_t before = a ? L.tile_end[a - 1] : 0;
     const uintptr_t p = reinterpret_cast<uintptr_t>(L.ptr[a]);
     const int64_t size = L.size[a];
@@ -56,10 +54,25 @@ __device__ __forceinline__ TileAt tile_at(const ListArgs &L, int count, uint32_t
     t.lo = (int64_t)(p & 15);
     t.hi = t.lo + (size >> 1);
     t.base = reinterpret_cast<char *>(p - (uintptr_t)t.lo);
-    t.first = (int64_t)(tile - before) * TILE;
-    t.nblk = (int)imin(TILE, ((t.hi + 15) >> 4) - t.first);
+    t.first = (int64_t)(tile - before) * blocks;
+    t.nblk = (int)imin(blocks, ((t.hi + 15) >> 4) - t.first);
     t.whole = 16 * t.first >= t.lo && 16 * (t.first + t.nblk) <= t.hi;
     return t;
+}
+
+// Find a workgroup's tile: a binary search in scalar registers.  It waits for
+// four to eight loads in turn, but costs few instructions and no vector
+// loads, and over a long list the wait does no harm: with the tensor found
+// in two loads (a table of hints) the 7B shard's norm took 492 us for 478,
+// with all ends compared at once in scalar or vector registers 492 and 500.
+template <int CAP>
+__device__ __forceinline__ TileAt tile_at(const ListArgs<CAP> &L, uint32_t tile, int blocks) {
+    int a = 0, b = CAP - 1;   // the first tensor whose tile_end lies above `tile`
+    while (a < b) {
+        const int mid = (a + b) >> 1;
+        if (L.tile_end[mid] <= tile) a = mid + 1; else b = mid;
+    }
+    return tile_of<CAP>(L, a, tile, blocks);
 }
 
 // Elements [*e_lo, *e_hi) of block b (of the tensor) lie inside the tensor.
@@ -71,9 +84,8 @@ __device__ __forceinline__ void block_range(const TileAt &t, int64_t b, int *e_l
 
 // ------------------------------------------------------------------ norm --
 
-constexpr int kNormUnroll = 8;                            // 16-byte blocks in flight per lane
-constexpr int kNormTile = kThreads * kNormUnroll;         // blocks of a tile (32 KB)
-constexpr int kNormWgs = 2048;                            // workgroups of a launch: each walks its share of the tiles
+constexpr int kNormUnroll = 2;                     // 16-byte blocks per lane
+constexpr int kNormTile = kThreads * kNormUnroll;  // blocks of a tile (8 KB): one per workgroup
 
 // bf16 lanes as fp32 bits
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -93,6 +105,18 @@ __device__ __forceinline__ void add_block(LaneTotal<KIND> &t, u32x4 v) {
     }
 }
 
+// Block b of the tile; elements outside the tensor are zero.
+template <int W>
+__device__ __forceinline__ u32x4 load_block(const TileAt &at, int b) {
+    u32x4 v = ld16(at.base + 16 * (at.first + b));
+    if (!at.whole) {
+        int e_lo, e_hi;
+        block_range<W>(at, at.first + b, &e_lo, &e_hi);
+        v &= elem_mask<W>(e_lo, e_hi);
+    }
+    return v;
+}
+
 template <int KIND, int W>
 __device__ __forceinline__ void add_tile(LaneTotal<KIND> &t, const TileAt &at) {
     u32x4 v[kNormUnroll];
@@ -100,63 +124,118 @@ __device__ __forceinline__ void add_tile(LaneTotal<KIND> &t, const TileAt &at) {
     for (int u = 0; u < kNormUnroll; ++u) {
         const int b = u * kThreads + threadIdx.x;
         v[u] = u32x4{0u, 0u, 0u, 0u};   // zeros add nothing to either total
-        if (b < at.nblk) {
-            v[u] = ld16(at.base + 16 * (at.first + b));
-            if (!at.whole) {
-                int e_lo, e_hi;
-                block_range<W>(at, at.first + b, &e_lo, &e_hi);
-                v[u] &= elem_mask<W>(e_lo, e_hi);
-            }
-        }
+        if (b < at.nblk) v[u] = load_block<W>(at, b);
     }
 #pragma unroll
     for (int u = 0; u < kNormUnroll; ++u) add_block<KIND, W>(t, v[u]);
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kThreads) void list_norm_kernel(ListArgs L, int count, uint32_t ntiles, double *parts) {
+template <int KIND, int CAP>
+__global__ __launch_bounds__(kThreads) void list_norm_kernel(ListArgs<CAP> L, double *parts) {
     __shared__ double lds[kThreads / 64];
     LaneTotal<KIND> t;
-    for (uint32_t tile = blockIdx.x; tile < ntiles; tile += gridDim.x) {
-        const TileAt at = tile_at<kNormTile>(L, count, tile);
-        if (at.f32) add_tile<KIND, 4>(t, at); else add_tile<KIND, 2>(t, at);
-    }
-    const double sum = norm_block_join<KIND, kThreads>(t.value(), lds);
+    const TileAt at = tile_at<CAP>(L, blockIdx.x, kNormTile);
+    if (at.f32) add_tile<KIND, 4>(t, at); else add_tile<KIND, 2>(t, at);
+    const double sum = norm_block_join<KIND, kThreads>(t, lds);
     if (threadIdx.x == 0) parts[blockIdx.x] = sum;
+}
+
+// A lane's part of parts[lo, hi): every THREADS-th, eight loads in flight.
+template <int KIND, int THREADS>
+__device__ __forceinline__ double join_parts(const double *__restrict__ parts, int64_t lo, int64_t hi) {
+    double t = 0;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 8 * THREADS) {
+        double v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = i + k * THREADS < hi ? parts[i + k * THREADS] : 0.0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t = norm_join<KIND>(t, v[k]);
+    }
+    return t;
 }
 
 // Many partial totals are first joined to kJoinWgs, each workgroup's in a
 // contiguous piece; one workgroup would read them at one CU's rate.
 constexpr int kJoinWgs = 512;
-constexpr int64_t kJoinMin = 8192;
+constexpr int64_t kJoinMin = 16384;
 
 template <int KIND>
 __global__ __launch_bounds__(kThreads) void norm_join_kernel(const double *__restrict__ parts, int64_t count,
                                                              double *__restrict__ out) {
     __shared__ double lds[kThreads / 64];
-    const int64_t lo = count * blockIdx.x / kJoinWgs, hi = count * (blockIdx.x + 1) / kJoinWgs;
-    double t = 0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) t = norm_join<KIND>(t, parts[i]);
+    double t = join_parts<KIND, kThreads>(parts, count * blockIdx.x / kJoinWgs, count * (blockIdx.x + 1) / kJoinWgs);
     t = norm_block_join<KIND, kThreads>(t, lds);
     if (threadIdx.x == 0) out[blockIdx.x] = t;
 }
 
-// Joins the partial totals in a fixed order; writes the total (joined to the
-// one that stands there, where the call accumulates) and the norm.
+// Thread 0 writes the total (joined to the one that stood there, where the
+// call accumulates) and the norm.
+template <int KIND>
+__device__ __forceinline__ void write_total(double t, double before, double *total, float *norm) {
+    if (threadIdx.x == 0) {
+        t = norm_join<KIND>(before, t);
+        total[0] = t;
+        if (norm) norm[0] = (float)norm_of(t, KIND == kInf);
+    }
+}
+
+// Joins the partial totals in a fixed order.
 constexpr int kFinishThreads = 1024;
 
 template <int KIND>
 __global__ __launch_bounds__(kFinishThreads) void norm_finish_kernel(const double *__restrict__ parts, int64_t count,
                                                                      int accumulate, double *total, float *norm) {
     __shared__ double lds[kFinishThreads / 64];
-    double t = 0;
-    for (int64_t i = threadIdx.x; i < count; i += kFinishThreads) t = norm_join<KIND>(t, parts[i]);
-    t = norm_block_join<KIND, kFinishThreads>(t, lds);
-    if (threadIdx.x == 0) {
-        if (accumulate) t = norm_join<KIND>(total[0], t);
-        total[0] = t;
-        if (norm) norm[0] = (float)norm_of(t, KIND == kInf);
+    const double before = accumulate ? total[0] : 0.0;
+    const double t = norm_block_join<KIND, kFinishThreads>(join_parts<KIND, kFinishThreads>(parts, 0, count), lds);
+    write_total<KIND>(t, before, total, norm);
+}
+
+// A short list in one launch: the waves of one workgroup take tiles of one
+// block per lane (1 KB) in turn, two of them in flight.
+// The launch and the workspace that it saves are about 4 us of a caller's
+// time; on the GPU it is ahead up to 80 KB (16 KB: 2.4 us for 3.9 of the two
+// launches; 64 KB: 3.3 for 3.9; 128 KB: 5.0 for 4.0; one wave's tiles follow
+// each other).
+constexpr int kOneTile = 64;
+constexpr int kOneUnroll = 2;
+constexpr int kOneMaxTiles = 128;
+
+template <int KIND, int CAP>
+__global__ __launch_bounds__(kFinishThreads) void list_norm_one_kernel(ListArgs<CAP> L, int ntiles, int accumulate,
+                                                                       double *total, float *norm) {
+    constexpr int kWaves = kFinishThreads / 64;
+    __shared__ double lds[kWaves];
+    const double before = accumulate ? total[0] : 0.0;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the tile ends, spread over the lanes: finding a tile then loads nothing
+    uint32_t end[(CAP + 63) / 64];
+#pragma unroll
+    for (int k = 0; k < (CAP + 63) / 64; ++k) end[k] = 64 * k + lane < CAP ? L.tile_end[64 * k + lane] : UINT32_MAX;
+    LaneTotal<KIND> t;
+    for (int first = wave; first < ntiles; first += kWaves * kOneUnroll) {
+        u32x4 v[kOneUnroll];
+        bool f32[kOneUnroll];
+#pragma unroll
+        for (int u = 0; u < kOneUnroll; ++u) {
+            v[u] = u32x4{0u, 0u, 0u, 0u};
+            f32[u] = false;
+            if (first + u * kWaves < ntiles) {
+                const uint32_t tile = first + u * kWaves;
+                int a = 0;
+#pragma unroll
+                for (int k = 0; k < (CAP + 63) / 64; ++k) a += __popcll(__ballot(end[k] <= tile));
+                const TileAt at = tile_of<CAP>(L, a, tile, kOneTile);
+                f32[u] = at.f32;
+                if (lane < at.nblk) v[u] = f32[u] ? load_block<4>(at, lane) : load_block<2>(at, lane);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kOneUnroll; ++u) {
+            if (f32[u]) add_block<KIND, 4>(t, v[u]); else add_block<KIND, 2>(t, v[u]);
+        }
     }
+    write_total<KIND>(norm_block_join<KIND, kFinishThreads>(t, lds), before, total, norm);
 }
 
 // ------------------------------------------------------------------ clip --
@@ -200,11 +279,12 @@ __device__ __forceinline__ void clip_tile(const TileAt &at, float c) {
     }
 }
 
-__global__ __launch_bounds__(kThreads) void list_clip_kernel(ListArgs L, int count, ClipArgs clip, float *norm) {
+template <int CAP>
+__global__ __launch_bounds__(kThreads) void list_clip_kernel(ListArgs<CAP> L, ClipArgs clip, float *norm) {
     const float c = clip_coef(clip);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)norm_of(clip.total[0], clip.inf);
-    if (c == 1.0f || count == 0) return;   // times one: the gradients stay as they are, unread
-    const TileAt at = tile_at<kClipTile>(L, count, blockIdx.x);
+    if (c == 1.0f || L.tile_end[0] == 0) return;   // times one: the gradients stay as they are, unread
+    const TileAt at = tile_at<CAP>(L, blockIdx.x, kClipTile);
     if (at.f32) clip_tile<4>(at, c); else clip_tile<2>(at, c);
 }
 
@@ -241,28 +321,52 @@ int check_list(const char *what, int32_t n_tensors, const void *const *grads, co
     return FS_OK;
 }
 
-// Cut the list into launches of at most kListMax tensors and call
-// f(args, tensors, tiles) for each; tensors without elements are left out.
-template <int TILE, class F>
-void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes, F &&f) {
-    ListArgs L;
+// Cut the list into launches of at most CAP tensors and call
+// f(args, tiles) for each; tensors without elements are left out.
+template <int CAP, class F>
+void launches_of(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes, int tile,
+                 F &&f) {
+    ListArgs<CAP> L;
     int count = 0;
     int64_t tiles = 0;
+    auto go = [&] {
+        for (int k = count; k < CAP; ++k) {
+            L.ptr[k] = nullptr;
+            L.size[k] = 0;
+            L.tile_end[k] = UINT32_MAX;
+        }
+        f(L, (uint32_t)tiles);
+        count = 0;
+        tiles = 0;
+    };
     for (int i = 0; i < n_tensors; ++i) {
         if (numel[i] == 0) continue;
-        if (count == kListMax) {
-            f(L, count, (uint32_t)tiles);
-            count = 0;
-            tiles = 0;
-        }
+        if (count == CAP) go();
         const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
-        tiles += tiles_of(grads[i], nb, TILE);
+        tiles += tiles_of(grads[i], nb, tile);
         L.ptr[count] = static_cast<char *>(const_cast<void *>(grads[i]));
         L.size[count] = nb * 2 + (dtypes[i] == FS_FP32);
         L.tile_end[count++] = (uint32_t)tiles;
     }
-    if (count) f(L, count, (uint32_t)tiles);
+    if (count) go();
 }
+
+template <class F>
+void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes, int tile,
+                     F &&f) {
+    // A call of few tensors copies a short list; one whose tensors without
+    // elements bring it down to few does not.
+    if (n_tensors <= kListFew)
+        launches_of<kListFew>(n_tensors, grads, numel, dtypes, tile, f);
+    else
+        launches_of<kListMax>(n_tensors, grads, numel, dtypes, tile, f);
+}
+
+// Whether the norm of `count` tensors (those with elements) goes in one launch.
+// A tensor's tiles are counted as if it started on the last byte of a block,
+// so that the choice and the workspace go by the sizes alone.
+const void *const anywhere = reinterpret_cast<const void *>(15);
+bool in_one_launch(int count, int64_t one_tiles) { return count <= kListMax && one_tiles <= kOneMaxTiles; }
 
 // Two tensors that share memory would be scaled twice, or raced on.
 int check_disjoint(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
@@ -345,13 +449,27 @@ int launch_norm_finish(const char *what, int type, int accumulate, double *parts
 
 }  // namespace fsi
 
+// Partial totals: one per tile; none where the list goes in one launch.
 extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, const fs_dtype *dtypes,
                                       int64_t *bytes) {
     clear_error();
-    if (!bytes) return fail(FS_E_INVAL, "fs_grad_norm_workspace: bytes is NULL");
-    if (n_tensors < 0) return fail(FS_E_INVAL, "fs_grad_norm_workspace: n_tensors < 0");
-    if (n_tensors > 0 && (!numel || !dtypes)) return fail(FS_E_INVAL, "fs_grad_norm_workspace: NULL list");
-    *bytes = norm_parts_bytes(((int64_t)n_tensors + kListMax - 1) / kListMax * kNormWgs);
+    const char *what = "fs_grad_norm_workspace";
+    if (!bytes) return fail(FS_E_INVAL, "%s: bytes is NULL", what);
+    if (n_tensors < 0) return fail(FS_E_INVAL, "%s: n_tensors < 0", what);
+    if (n_tensors > 0 && (!numel || !dtypes)) return fail(FS_E_INVAL, "%s: NULL list", what);
+    int64_t tiles = 0, one_tiles = 0;
+    int count = 0;
+    for (int i = 0; i < n_tensors; ++i) {
+        if (numel[i] < 0) return fail(FS_E_INVAL, "%s: tensor %d has a negative element count", what, i);
+        if (numel[i] > (INT64_MAX >> 4)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large", what, i);
+        if (numel[i] == 0) continue;
+        const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
+        tiles += tiles_of(anywhere, nb, kNormTile);
+        one_tiles = std::min<int64_t>(one_tiles + tiles_of(anywhere, nb, kOneTile), INT32_MAX);
+        ++count;
+        if (tiles > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+    }
+    *bytes = in_one_launch(count, one_tiles) ? 0 : norm_parts_bytes(tiles);
     return FS_OK;
 }
 
@@ -359,12 +477,13 @@ namespace {
 
 int check_grad_norm(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
                     const fs_dtype *dtypes, fs_norm_type type, const double *total, const float *norm,
-                    const void *workspace, size_t bytes) {
+                    const void *workspace, size_t bytes, int64_t *need_out) {
     if (int rc = check_norm_out(what, type, total, norm)) return rc;
     if (int rc = check_list(what, n_tensors, grads, numel, dtypes, kNormTile, total, norm)) return rc;
     int64_t need = 0;
     if (int rc = fs_grad_norm_workspace(n_tensors, numel, dtypes, &need)) return rc;
     if (int rc = check_workspace_range(what, workspace, bytes, need, total, norm)) return rc;
+    *need_out = need;
     for (int i = 0; i < n_tensors; ++i)
         if (ranges_overlap(workspace, need, grads[i], numel[i] * elem_bytes(dtypes[i])))
             return fail(FS_E_INVAL, "%s: workspace overlaps tensor %d", what, i);
@@ -378,19 +497,35 @@ extern "C" int fs_grad_norm(int32_t n_tensors, const void *const *grads, const i
                             size_t bytes, hipStream_t stream) {
     clear_error();
     const char *what = "fs_grad_norm";
-    if (int rc = check_grad_norm(what, n_tensors, grads, numel, dtypes, type, total, norm, workspace, bytes)) return rc;
+    int64_t need = 0;
+    if (int rc = check_grad_norm(what, n_tensors, grads, numel, dtypes, type, total, norm, workspace, bytes, &need))
+        return rc;
     (void)hipGetLastError();
+    if (need == 0) {   // one launch, which also covers an empty list
+        bool empty = true;
+        auto one = [&](const auto &L, uint32_t tiles) {
+            constexpr int kCap = sizeof(L.ptr) / sizeof(L.ptr[0]);
+            empty = false;
+            if (type == FS_NORM_L2)
+                hipLaunchKernelGGL((list_norm_one_kernel<kL2, kCap>), dim3(1), dim3(kFinishThreads), 0, stream, L,
+                                   (int)tiles, accumulate != 0, total, norm);
+            else
+                hipLaunchKernelGGL((list_norm_one_kernel<kInf, kCap>), dim3(1), dim3(kFinishThreads), 0, stream, L,
+                                   (int)tiles, accumulate != 0, total, norm);
+        };
+        for_each_launch(n_tensors, grads, numel, dtypes, kOneTile, one);
+        if (!empty) return check_launch(what);
+        return launch_norm_finish(what, type, accumulate != 0, nullptr, 0, total, norm, stream);
+    }
     double *parts = static_cast<double *>(workspace);
     int64_t count = 0;
-    for_each_launch<kNormTile>(n_tensors, grads, numel, dtypes, [&](const ListArgs &L, int tensors, uint32_t tiles) {
-        const uint32_t grid = std::min<uint32_t>(kNormWgs, tiles);
+    for_each_launch(n_tensors, grads, numel, dtypes, kNormTile, [&](const auto &L, uint32_t tiles) {
+        constexpr int kCap = sizeof(L.ptr) / sizeof(L.ptr[0]);
         if (type == FS_NORM_L2)
-            hipLaunchKernelGGL(list_norm_kernel<kL2>, dim3(grid), dim3(kThreads), 0, stream, L, tensors, tiles,
-                               parts + count);
+            hipLaunchKernelGGL((list_norm_kernel<kL2, kCap>), dim3(tiles), dim3(kThreads), 0, stream, L, parts + count);
         else
-            hipLaunchKernelGGL(list_norm_kernel<kInf>, dim3(grid), dim3(kThreads), 0, stream, L, tensors, tiles,
-                               parts + count);
-        count += grid;
+            hipLaunchKernelGGL((list_norm_kernel<kInf, kCap>), dim3(tiles), dim3(kThreads), 0, stream, L, parts + count);
+        count += tiles;
     });
     if (int rc = check_launch(what)) return rc;
     return launch_norm_finish(what, type, accumulate != 0, parts, count, total, norm, stream);
@@ -407,14 +542,15 @@ extern "C" int fs_clip_grads(int32_t n_tensors, void *const *grads, const int64_
     if (int rc = check_disjoint(what, n_tensors, grads, numel, dtypes)) return rc;
     (void)hipGetLastError();
     float *out = norm;   // the first launch writes it
-    for_each_launch<kClipTile>(n_tensors, grads, numel, dtypes, [&](const ListArgs &L, int tensors, uint32_t tiles) {
-        hipLaunchKernelGGL(list_clip_kernel, dim3(tiles), dim3(kThreads), 0, stream, L, tensors, c, out);
+    for_each_launch(n_tensors, grads, numel, dtypes, kClipTile, [&](const auto &L, uint32_t tiles) {
+        constexpr int kCap = sizeof(L.ptr) / sizeof(L.ptr[0]);
+        hipLaunchKernelGGL(list_clip_kernel<kCap>, dim3(tiles), dim3(kThreads), 0, stream, L, c, out);
         out = nullptr;
     });
     if (out) {   // no tensor has elements
-        ListArgs none;
+        ListArgs<kListFew> none;
         memset(&none, 0, sizeof none);
-        hipLaunchKernelGGL(list_clip_kernel, dim3(1), dim3(kThreads), 0, stream, none, 0, c, out);
+        hipLaunchKernelGGL(list_clip_kernel<kListFew>, dim3(1), dim3(kThreads), 0, stream, none, c, out);
     }
     return check_launch(what);
 }
