@@ -240,8 +240,15 @@ __global__ __launch_bounds__(kFinishThreads) void list_norm_one_kernel(ListArgs<
 
 // ------------------------------------------------------------------ clip --
 
-constexpr int kClipUnroll = 4;
-constexpr int kClipTile = kThreads * kClipUnroll;   // blocks of a tile (16 KB): one per workgroup
+// One tile per workgroup.  Over the 7B shard (3.37 GB in fp32, 1.68 in bf16)
+// and 97 odd tensors of both types, 118 MB: 128 threads with two blocks each
+// 1050 / 515 / 41.3 us, 64 threads with one block 1014 / 561 / 45.1, 256 with
+// four 1102 / 586 / 44.8; workgroups that walk several tiles 1034 to 1340,
+// residency caps 1045 to 1690.  A call whose coefficient is 1 costs its
+// workgroups' launches, 183 us over the 7B shard.
+constexpr int kClipThreads = 128;
+constexpr int kClipUnroll = 2;
+constexpr int kClipTile = kClipThreads * kClipUnroll;   // 16-byte blocks of a tile (4 KB)
 
 template <int W>
 __device__ __forceinline__ u32x4 scale_block(u32x4 v, float c) {
@@ -261,12 +268,12 @@ __device__ __forceinline__ void clip_tile(const TileAt &at, float c) {
     u32x4 v[kClipUnroll];
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
-        const int b = u * kThreads + threadIdx.x;
+        const int b = u * kClipThreads + threadIdx.x;
         if (b < at.nblk) v[u] = ld16(at.base + 16 * (at.first + b));
     }
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
-        const int b = u * kThreads + threadIdx.x;
+        const int b = u * kClipThreads + threadIdx.x;
         if (b >= at.nblk) continue;
         char *p = at.base + 16 * (at.first + b);
         const u32x4 x = scale_block<W>(v[u], c);
@@ -280,7 +287,7 @@ __device__ __forceinline__ void clip_tile(const TileAt &at, float c) {
 }
 
 template <int CAP>
-__global__ __launch_bounds__(kThreads) void list_clip_kernel(ListArgs<CAP> L, ClipArgs clip, float *norm) {
+__global__ __launch_bounds__(kClipThreads) void list_clip_kernel(ListArgs<CAP> L, ClipArgs clip, float *norm) {
     const float c = clip_coef(clip);
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) norm[0] = (float)norm_of(clip.total[0], clip.inf);
     if (c == 1.0f || L.tile_end[0] == 0) return;   // times one: the gradients stay as they are, unread
@@ -544,13 +551,13 @@ extern "C" int fs_clip_grads(int32_t n_tensors, void *const *grads, const int64_
     float *out = norm;   // the first launch writes it
     for_each_launch(n_tensors, grads, numel, dtypes, kClipTile, [&](const auto &L, uint32_t tiles) {
         constexpr int kCap = sizeof(L.ptr) / sizeof(L.ptr[0]);
-        hipLaunchKernelGGL(list_clip_kernel<kCap>, dim3(tiles), dim3(kThreads), 0, stream, L, c, out);
+        hipLaunchKernelGGL(list_clip_kernel<kCap>, dim3(tiles), dim3(kClipThreads), 0, stream, L, c, out);
         out = nullptr;
     });
     if (out) {   // no tensor has elements
         ListArgs<kListFew> none;
         memset(&none, 0, sizeof none);
-        hipLaunchKernelGGL(list_clip_kernel<kListFew>, dim3(1), dim3(kThreads), 0, stream, none, c, out);
+        hipLaunchKernelGGL(list_clip_kernel<kListFew>, dim3(1), dim3(kClipThreads), 0, stream, none, c, out);
     }
     return check_launch(what);
 }
