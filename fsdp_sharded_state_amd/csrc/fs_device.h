@@ -95,10 +95,10 @@ inline CuLimits cu_limits() {
 
 // Dynamic LDS bytes for a grid of `grid` workgroups capped at k per CU, for a
 // kernel that already uses `static_bytes` of LDS (0: no cap).
-inline uint32_t lds_cap(int k, int64_t grid, int64_t static_bytes = 0) {
+inline uint32_t lds_cap(int k, int64_t grid, int64_t static_bytes = 0, int64_t min_rounds = kCapMinRounds) {
     const CuLimits L = cu_limits();
     if (L.lds_per_cu <= 0 || k < 1) return 0;
-    if (grid < kCapMinRounds * k * (int64_t)L.cus) return 0;
+    if (grid < min_rounds * k * (int64_t)L.cus) return 0;
     const int64_t per_wg = L.lds_per_cu / (k + 1) + 1;   // k of these fit in a CU, k + 1 do not
     if (per_wg > L.lds_per_wg || per_wg * k > L.lds_per_cu || per_wg <= static_bytes) return 0;
     return (uint32_t)(per_wg - static_bytes);

@@ -485,13 +485,14 @@ __device__ __forceinline__ u32x4 ld_slice16(const uint16_t *p, int64_t off) {
     return funnel16(lo, hi, sh);
 }
 
-// Each wave writes its partial total.  One per wave, with no barrier: at
-// one to three workgroups per CU the waves of a workgroup should not wait for
-// each other.
+// The workgroup's partial total.  (One per wave, without the barrier, was
+// slower: four times as many to join, 83.8 us against 81.9 on one 7B block's
+// 8-term reduce and 813 against 795 on 32 slices of 75.9M elements.)
 template <int KIND>
-__device__ __forceinline__ void store_wave_total(const LaneTotal<KIND> &t, double *__restrict__ parts) {
-    const double sum = norm_wave_join<KIND>(t);
-    if ((threadIdx.x & 63) == 63) parts[(int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)] = sum;
+__device__ __forceinline__ void store_total(const LaneTotal<KIND> &t, double *__restrict__ parts) {
+    __shared__ double lds[kThreads / 64];
+    const double sum = norm_block_join<KIND, kThreads>(t, lds);
+    if (threadIdx.x == 0) parts[blockIdx.x] = sum;
 }
 
 // Misaligned slices or output: lane i owns 8 consecutive elements, one
@@ -551,15 +552,32 @@ __global__ __launch_bounds__(kThreads) void reduce_general_kernel(SliceArgs sa, 
         out[e] = acc;
         if (KIND) total.add(acc);
     }
-    if (KIND) store_wave_total<KIND>(total, parts);
+    if (KIND) store_total<KIND>(total, parts);
 }
 
 constexpr int kRedGroupsMany = 16;                                      // passes of > kRedFewTerms terms
 constexpr int kRedGroupsFew = 4;                                        // passes of <= kRedFewTerms terms
 constexpr int kRedFewTerms = 16;
 constexpr int64_t kWgRow = (int64_t)kThreads * 4;                       // elements of one group index across a workgroup
+constexpr int kRedSlicesMany = 2;                                       // slices in flight
+constexpr int kRedSlicesFew = 1;
 constexpr int64_t kRedChunk = kWgRow * kRedGroupsMany;                  // 16384 elements
 constexpr int64_t kRedChunkFew = kWgRow * kRedGroupsFew;                // 4096 elements
+
+// Shapes of fs_reduce_shard_norm's chunks by the call's length; 16-term and
+// longer passes gain most from them.  Short calls (below kRedShort elements)
+// leave CUs idle in chunks of 4096 or 16384 elements, and wait for each slice
+// in turn: in chunks of 2048 with eight slices in flight, 32 terms of 64K
+// elements take 11.3 us for 30.2, of 1M 16.9 for 32.8, of 2M 29.2 for 36.4 (of
+// 4M 54.9 for 46.5).  Up to kRedManyMin elements the chunks of 16384 make few
+// rounds of one workgroup per CU: 32 terms of 25.3M elements take 275 us for
+// 326 in chunks of 4096, of 50M 520 for 637, of 75.9M 801 for 850 (of 210M
+// 2212 for 2158).  The residency cap of the chunks of 4096 helps from 50M
+// elements on (556 us without it), kNormCapRounds rounds.
+constexpr int kRedGroupsShort = 2, kRedSlicesShort = 8;
+constexpr int64_t kRedShort = 1 << 21;
+constexpr int64_t kRedManyMin = 1 << 27;
+constexpr int64_t kNormCapRounds = 12;
 
 __device__ __forceinline__ void f4(u32x4 v, float o[4]) {
     o[0] = __uint_as_float(v.x);
@@ -682,14 +700,14 @@ __device__ __forceinline__ void sum_slices(const SliceArgs &sa, int nterms, bool
     }
 }
 
-template <int KIND, int G, bool TAIL>
+template <int KIND, int G, int SL, bool TAIL>
 __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, int first_pass, int last_pass,
                                              float world, float *__restrict__ out, LaneTotal<KIND> &lane_total,
                                              int64_t base, int64_t n) {
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G];
     if (!first_pass) load_f32_groups<G, G, TAIL>(acc, out, base, B);   // partial sums of the earlier passes
-    sum_slices<G, (G >= 16 ? 2 : 1), TAIL>(sa, nterms, first_pass, acc, base, B);   // slices in flight
+    sum_slices<G, SL, TAIL>(sa, nterms, first_pass, acc, base, B);
     if (last_pass) {
 #pragma unroll
         for (int e = 0; e < 4 * G; ++e) acc[e] = acc[e] / world;
@@ -718,17 +736,17 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
 
 // KIND: kNoNorm, or (in the last pass) the norm whose partial totals, one per
 // wave, go to `parts`.
-template <int KIND, int G>
+template <int KIND, int G, int SL>
 __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, int nterms, int first_pass,
                                                                 int last_pass, float world,
                                                                 float *__restrict__ out, int64_t n,
                                                                 double *__restrict__ parts) {
-    static_assert(G % kTailGroups == 0, "the tail walks whole sub-chunks");
+    static_assert(G % kTailGroups == 0 || G < kTailGroups, "the tail walks whole sub-chunks, or lies inside one");
     LaneTotal<KIND> t;
-    FS_CHUNK_DISPATCH(G, (reduce_chunk<KIND, G, false>(sa, nterms, first_pass, last_pass, world, out, t, base, n)),
-                      (reduce_chunk<KIND, kTailGroups, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
+    FS_CHUNK_DISPATCH(G, (reduce_chunk<KIND, G, SL, false>(sa, nterms, first_pass, last_pass, world, out, t, base, n)),
+                      (reduce_chunk<KIND, kTailGroups, SL, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
                                                              n)));
-    if (KIND) store_wave_total<KIND>(t, parts);
+    if (KIND) store_total<KIND>(t, parts);
 }
 
 // ------------------------------------------------- bf16 reduce dtype --
@@ -809,7 +827,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_chunk_kernel(SliceArgs sa,
     FS_CHUNK_DISPATCH(G, (reduce_rs_chunk<KIND, G, false>(sa, nsteps, world, first_pass, worldf, out, t, base, n)),
                       (reduce_rs_chunk<KIND, kTailGroups, true>(sa, nsteps, world, first_pass, worldf, out, t, base,
                                                                 n)));
-    if (KIND) store_wave_total<KIND>(t, parts);
+    if (KIND) store_total<KIND>(t, parts);
 }
 
 // Misaligned variant: 8 elements per lane, element tail.
@@ -857,7 +875,7 @@ __global__ __launch_bounds__(kThreads) void reduce_rs_general_kernel(SliceArgs s
         out[e] = acc;
         if (KIND) total.add(acc);
     }
-    if (KIND) store_wave_total<KIND>(total, parts);
+    if (KIND) store_total<KIND>(total, parts);
 }
 
 // ----------------------------------------------------------------- AdamW --
@@ -1316,19 +1334,24 @@ void launch_reduce_pass(int64_t n, int64_t off, int64_t len, hipStream_t stream,
     double *parts = np ? np->next : nullptr;
     int64_t grid;
     if (aligned) {
-        const bool few = cnt <= kRedFewTerms;
-        const int64_t chunk = few ? kRedChunkFew : kRedChunk;
+        const bool is_short = np && n < kRedShort, few = cnt <= kRedFewTerms || (np && n < kRedManyMin);
+        const int64_t chunk = is_short ? kWgRow * kRedGroupsShort : few ? kRedChunkFew : kRedChunk;
         grid = (len + chunk - 1) / chunk;
         const dim3 g((uint32_t)grid);
-        const uint32_t lds = lds_cap(few ? kRedFewWgsPerCu : kRedManyWgsPerCu, (n + chunk - 1) / chunk);
+        const uint32_t lds = lds_cap(few ? kRedFewWgsPerCu : kRedManyWgsPerCu, (n + chunk - 1) / chunk,
+                                     np ? (kThreads / 64) * (int64_t)sizeof(double) : 0,
+                                     np ? kNormCapRounds : kCapMinRounds);
         with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
             constexpr int kKind = decltype(kind)::value;
-            if (few)
-                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsFew>), g, dim3(kThreads), lds, stream, sa,
-                                   cnt, first, last, world, o, len, parts);
+            if (is_short)
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsShort, kRedSlicesShort>), g, dim3(kThreads), 0,
+                                   stream, sa, cnt, first, last, world, o, len, parts);
+            else if (few)
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsFew, kRedSlicesFew>), g, dim3(kThreads), lds,
+                                   stream, sa, cnt, first, last, world, o, len, parts);
             else
-                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsMany>), g, dim3(kThreads), lds, stream, sa,
-                                   cnt, first, last, world, o, len, parts);
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsMany, kRedSlicesMany>), g, dim3(kThreads),
+                                   lds, stream, sa, cnt, first, last, world, o, len, parts);
         });
     } else {
         grid = std::max<int64_t>(1, ((len >> 3) + kThreads - 1) / kThreads);
@@ -1337,7 +1360,7 @@ void launch_reduce_pass(int64_t n, int64_t off, int64_t len, hipStream_t stream,
                                stream, sa, cnt, first, last, world, len, o, parts);
         });
     }
-    if (np && last) np->next += grid * (kThreads / 64);
+    if (np && last) np->next += grid;
 }
 
 // Largest grid any launch over n elements needs: one workgroup per kAdamRow
@@ -1639,7 +1662,7 @@ int run_reduce_rs(const char *what, int64_t n, int32_t world, int32_t grad_acc, 
                                        parts);
                 });
             }
-            if (np && last) np->next += grid * (kThreads / 64);
+            if (np && last) np->next += grid;
             int rc = check_launch(what);
             if (rc != FS_OK) return rc;
         }
@@ -1678,18 +1701,17 @@ extern "C" int fs_reduce_shard_ex(int64_t n, int32_t world, int32_t grad_acc, fs
     return run_reduce_rs("fs_reduce_shard_ex", n, world, grad_acc, slices, out, aligned, stream, nullptr);
 }
 
-// Partial totals: one per wave of every workgroup of the last pass's
-// launches.  The smallest chunk is the general kernels' (kThreads * 8
-// elements); launch spans are multiples of every chunk.
+// Partial totals: one per workgroup of the last pass's launches.  Launch spans
+// are multiples of every chunk.
 extern "C" int fs_reduce_shard_norm_workspace(int64_t n, int64_t *bytes) {
     fsi::clear_error();
     if (!bytes) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: bytes is NULL");
     if (n < 0) return fsi::fail(FS_E_INVAL, "fs_reduce_shard_norm_workspace: n < 0");
-    constexpr int64_t kChunk = kThreads * 8;
-    static_assert(kSpan % kChunk == 0 && kRsSpan % kChunk == 0 && kRedChunkFew >= kChunk && kWgRow * kRsGroupsFew >= kChunk,
+    constexpr int64_t kChunk = kThreads * 8;   // the smallest: the general kernels' and the short calls'
+    static_assert(kSpan % kChunk == 0 && kRsSpan % kChunk == 0 && kWgRow * kRedGroupsShort >= kChunk &&
+                      kRedChunkFew >= kChunk && kWgRow * kRsGroupsFew >= kChunk,
                   "the workspace counts chunks of kChunk elements");
-    const int64_t waves = (n / kChunk + (n % kChunk != 0)) * (kThreads / 64);
-    *bytes = norm_parts_bytes(waves);
+    *bytes = norm_parts_bytes(n / kChunk + (n % kChunk != 0));
     return FS_OK;
 }
 

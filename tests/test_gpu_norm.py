@@ -253,6 +253,28 @@ def test_reduce_norm(n, N, A, shift, rd, norm_type):
     assert float(total) == (2 * before if norm_type == 2 else before)
 
 
+@pytest.mark.parametrize("n,terms", [(2_100_003, 32), (2_100_003, 40), ((1 << 21) - 1, 24), (5_000_011, 17), ((1 << 27) + 4099, 17)])
+def test_reduce_norm_in_every_chunk_shape(n, terms):
+    """The shapes that go by length and term count; the slices are 17 to 40
+    windows of one buffer, 8 elements apart."""
+    say("reduce norm shapes", n, terms)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    buf = torch.empty(n + 8 * terms, dtype=BF, device="cuda")
+    for piece in buf.split(1 << 24):
+        piece.copy_(torch.randn(piece.numel(), generator=g, device="cuda").mul_(1e-3))
+    sl = [buf[8 * k:8 * k + n] for k in range(terms)]
+    out, plain = torch.full((n,), 9.0, device="cuda"), torch.empty(n, device="cuda")
+    total, norm = scalars()
+    fs.fs_reduce_shard_norm(sl, out, total, norm, world=terms)
+    fs.fs_reduce_shard(sl, plain, terms)
+    assert torch.equal(out, plain)
+    want = sum(float(torch.dot(p, p)) for p in (q.double() for q in plain.split(1 << 24)))
+    assert abs(float(total) - want) <= 2 * ref.total_tol(n) * want
+    ref.check_norm(norm, float(total), 2)
+    fs.fs_reduce_shard_norm(sl, out, total, norm, world=terms, norm_type=math.inf)
+    assert float(total) == float(plain.abs().max())
+
+
 @pytest.mark.parametrize("rd", ["fp32", "bf16"])
 def test_reduce_norm_over_launch_spans(rd):
     """Longer than two launch spans, 33 terms in two passes for fp32, a ragged end."""
