@@ -559,6 +559,7 @@ def fs_reduce_adamw_step_noalloc(slices: Sequence[torch.Tensor], master: torch.T
                                               ptr(param_bf16, "param_bf16"), ctypes.byref(hp), _stream(stream)))
 
 
+_DTYPE_CODES = {torch.bfloat16: FS_BF16, torch.float32: FS_FP32}
 _NORM_CODES = {2: FS_NORM_L2, "2": FS_NORM_L2, math.inf: FS_NORM_INF, "inf": FS_NORM_INF}
 
 
@@ -579,22 +580,24 @@ class GradList:
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         n = len(tensors)
-        ptrs, numels, codes, index, storages = [], [], [], None, {}
+        index = tensors[0].get_device() if n else None
+        ptrs, numels, codes, storages = [], [], [], {}
         for i, t in enumerate(tensors):
-            ptrs.append(_dev_ptr(t, f"tensor {i}"))
-            numels.append(t.numel())
-            codes.append(_dtype_code(t.dtype))
-            if index is None:
-                index = t.get_device()
-            elif t.get_device() != index:
+            if not t.is_cuda or not t.is_contiguous():
+                _dev_ptr(t, f"tensor {i}")      # raises
+            if t.get_device() != index:
                 raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {tensors[0].device}")
+            ptrs.append(t.data_ptr())
+            numels.append(t.numel())
+            code = _DTYPE_CODES.get(t.dtype)
+            codes.append(_dtype_code(t.dtype) if code is None else code)
             st = t.untyped_storage()
-            storages[st.data_ptr()] = (st, st.data_ptr(), st.nbytes())
-        self._index: Optional[int] = index          # of their GPU; None for an empty list
-        self.numels, self.codes = numels, codes
+            at = st.data_ptr()
+            if at not in storages:
+                storages[at] = (st, at, st.nbytes())    # holding the storage keeps the memory
+        self._index: Optional[int] = index              # of their GPU; None for an empty list
         self._same = (codes[0], numels[0]) if n and len(set(codes)) == 1 and len(set(numels)) == 1 else None
         self._storages = list(storages.values())
-        self._tensors = [t.detach() for t in tensors]   # aliases: they keep the memory
         self._n = n
         self._ptrs = (ctypes.c_void_p * max(1, n))(*ptrs)
         self._numels = (ctypes.c_int64 * max(1, n))(*numels)
@@ -602,6 +605,9 @@ class GradList:
         need = ctypes.c_int64()
         _check(lib().fs_grad_norm_workspace(n, self._numels, self._codes, ctypes.byref(need)))
         self._norm_bytes = need.value
+        if self._same is not None:
+            _check(lib().fs_reduce_shard_norm_workspace(numels[0], ctypes.byref(need)))
+        self._reduce_bytes = need.value                 # as the slices of one reduce
 
     def __len__(self) -> int:
         return self._n
@@ -642,7 +648,7 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
     that GPU's current stream).  scratch >= 0: that many workspace bytes and
     their count go before the stream; they belong to the stream the kernels
     run on, so the allocator hands them out again in that stream's order."""
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _launch(index, stream, fn, *args, scratch=scratch)
     if stream is None:
@@ -655,10 +661,10 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
         return _check(fn(*args, handle))
     if scratch == 0:
         return _check(fn(*args, None, 0, handle))
-    device = torch.device("cuda", index)
     if stream is None:
-        ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+        ws = torch.empty(scratch, dtype=torch.uint8, device=index)
     else:
+        device = torch.device("cuda", index)
         own = (stream if isinstance(stream, torch.cuda.Stream) else
                torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
         with torch.cuda.stream(own):
@@ -710,11 +716,9 @@ def fs_reduce_shard_norm(slices, out: torch.Tensor, total: torch.Tensor, norm: O
     if gl._n and gl._index != index:
         raise ValueError(f"fs_reduce_shard_norm: out is on {out.device}, the slices on cuda:{gl._index}")
     ptr = _dev_ptr(out, "out")
-    need = ctypes.c_int64()
-    _check(lib().fs_reduce_shard_norm_workspace(n, ctypes.byref(need)))
     _launch(index, stream, lib().fs_reduce_shard_norm, n, int(world), int(grad_acc), _dtype_code(reduce_dtype),
             gl._ptrs, ptr if n else 0, kind, int(accumulate), _scalar_ptr(total, torch.float64, index, "total"),
-            _scalar_ptr(norm, torch.float32, index, "norm"), scratch=need.value)
+            _scalar_ptr(norm, torch.float32, index, "norm"), scratch=gl._reduce_bytes)
 
 
 def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: torch.Tensor, grad: torch.Tensor,

@@ -567,14 +567,16 @@ constexpr int64_t kRedChunkFew = kWgRow * kRedGroupsFew;                // 4096 
 // Shapes of fs_reduce_shard_norm's chunks by the call's length; 16-term and
 // longer passes gain most from them.  Short calls (below kRedShort elements)
 // leave CUs idle in chunks of 4096 or 16384 elements, and wait for each slice
-// in turn: in chunks of 2048 with eight slices in flight, 32 terms of 64K
-// elements take 11.3 us for 30.2, of 1M 16.9 for 32.8, of 2M 29.2 for 36.4 (of
-// 4M 54.9 for 46.5).  Up to kRedManyMin elements the chunks of 16384 make few
-// rounds of one workgroup per CU: 32 terms of 25.3M elements take 275 us for
-// 326 in chunks of 4096, of 50M 520 for 637, of 75.9M 801 for 850 (of 210M
-// 2212 for 2158).  The residency cap of the chunks of 4096 helps from 50M
-// elements on (556 us without it), kNormCapRounds rounds.
-constexpr int kRedGroupsShort = 2, kRedSlicesShort = 8;
+// and its pointer in turn: in chunks of 2048 with two batches of four slices
+// in flight, 32 terms of 64K elements take 8.3 us for 30.2, of 1M 16.4 for
+// 32.8, of 2M 29.2 for 36.4 (of 4M 58.8 for 46.5; batches of eight: 7.9,
+// 16.0, 29.7, 60.6, and 4.9 for 4.3 us on 4 terms of 1K).  Up to kRedManyMin
+// elements the chunks of 16384 make few rounds of one workgroup per CU: 32
+// terms of 25.3M elements take 275 us for 326 in chunks of 4096, of 50M 520
+// for 637, of 75.9M 801 for 850 (of 210M 2212 for 2158).  The residency cap of
+// the chunks of 4096 helps from 50M elements on (556 us without it),
+// kNormCapRounds rounds.
+constexpr int kRedGroupsShort = 2, kRedSlicesShort = 4;
 constexpr int64_t kRedShort = 1 << 21;
 constexpr int64_t kRedManyMin = 1 << 27;
 constexpr int64_t kNormCapRounds = 12;
@@ -700,6 +702,44 @@ __device__ __forceinline__ void sum_slices(const SliceArgs &sa, int nterms, bool
     }
 }
 
+// The same sum, SL slices at a time: a batch's pointers arrive in one scalar
+// load, and the next batch's loads go out before the current one is added.
+// Dead groups read the buffer's first block, so no load waits for a branch;
+// their sums are not used.
+template <int G, int SL, bool TAIL>
+__device__ __forceinline__ void sum_batches(const SliceArgs &sa, int nterms, bool init, float *acc, int64_t base,
+                                            const Bounds<G, TAIL> &B) {
+    u32x2 x[2][SL][G];
+    auto load = [&](u32x2 (&b)[SL][G], int t0) {
+#pragma unroll
+        for (int k = 0; k < SL; ++k)
+            if (t0 + k < nterms) {
+#pragma unroll
+                for (int u = 0; u < G; ++u)
+                    b[k][u] = __builtin_nontemporal_load(
+                        reinterpret_cast<const u32x2 *>(sa.p[t0 + k] + (B.live(u) ? base + u * kWgRow : 0)));
+            }
+    };
+    auto add = [&](const u32x2 (&b)[SL][G], int t0) {
+#pragma unroll
+        for (int k = 0; k < SL; ++k) {
+            if (t0 + k >= nterms) break;
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                if (k == 0 && t0 == 0 && init) set_bf16x4(acc + 4 * u, b[k][u]);
+                else add_bf16x4(acc + 4 * u, b[k][u]);
+            }
+        }
+    };
+    load(x[0], 0);
+    for (int t0 = 0; t0 < nterms; t0 += 2 * SL) {
+        load(x[1], t0 + SL);
+        add(x[0], t0);
+        load(x[0], t0 + 2 * SL);
+        add(x[1], t0 + SL);
+    }
+}
+
 template <int KIND, int G, int SL, bool TAIL>
 __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, int first_pass, int last_pass,
                                              float world, float *__restrict__ out, LaneTotal<KIND> &lane_total,
@@ -707,7 +747,8 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
     const Bounds<G, TAIL> B(base, n);
     float acc[4 * G];
     if (!first_pass) load_f32_groups<G, G, TAIL>(acc, out, base, B);   // partial sums of the earlier passes
-    sum_slices<G, SL, TAIL>(sa, nterms, first_pass, acc, base, B);
+    if constexpr (SL >= 4) sum_batches<G, SL, TAIL>(sa, nterms, first_pass, acc, base, B);
+    else sum_slices<G, SL, TAIL>(sa, nterms, first_pass, acc, base, B);
     if (last_pass) {
 #pragma unroll
         for (int e = 0; e < 4 * G; ++e) acc[e] = acc[e] / world;
@@ -720,6 +761,8 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
 // The chunk of workgroup blockIdx.x: whole, or the last one cut by n (walked
 // in sub-chunks of kTailGroups groups).  `body(groups_tag, base, tail)` runs
 // one (sub-)chunk.
+constexpr int tail_groups(int g) { return g < kTailGroups ? g : kTailGroups; }
+
 #define FS_CHUNK_DISPATCH(G, FULL_CALL, TAIL_CALL)                                               \
     do {                                                                                        \
         const int64_t chunk_lo = (int64_t)blockIdx.x * (kWgRow * (G));                         \
@@ -727,7 +770,7 @@ __device__ __forceinline__ void reduce_chunk(const SliceArgs &sa, int nterms, in
             const int64_t base = chunk_lo + 4 * threadIdx.x;                                    \
             FULL_CALL;                                                                          \
         } else {                                                                                \
-            for (int64_t sub = chunk_lo; sub < n; sub += kWgRow * kTailGroups) {                \
+            for (int64_t sub = chunk_lo; sub < n; sub += kWgRow * tail_groups(G)) {             \
                 const int64_t base = sub + 4 * threadIdx.x;                                     \
                 TAIL_CALL;                                                                      \
             }                                                                                   \
@@ -741,12 +784,58 @@ __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, in
                                                                 int last_pass, float world,
                                                                 float *__restrict__ out, int64_t n,
                                                                 double *__restrict__ parts) {
-    static_assert(G % kTailGroups == 0 || G < kTailGroups, "the tail walks whole sub-chunks, or lies inside one");
+    static_assert(G % tail_groups(G) == 0, "the tail walks whole sub-chunks");
     LaneTotal<KIND> t;
     FS_CHUNK_DISPATCH(G, (reduce_chunk<KIND, G, SL, false>(sa, nterms, first_pass, last_pass, world, out, t, base, n)),
-                      (reduce_chunk<KIND, kTailGroups, SL, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
+                      (reduce_chunk<KIND, tail_groups(G), SL, true>(sa, nterms, first_pass, last_pass, world, out, t, base,
                                                              n)));
     if (KIND) store_total<KIND>(t, parts);
+}
+
+// A tiny reduce with its norm in one launch of one workgroup: the launch and
+// the workspace that it saves are worth 3 us of a caller's time.  On the GPU
+// it takes 2.4 us for 4.3 (4 terms of 1K elements), 3.5 for 4.4 (of 8K), 4.4
+// for 6.9 (32 terms of 1K); at twice kOneMaxReads it is slower.  A lane owns
+// groups of 4 elements, 4 * kOneThreads apart; a group that n cuts is read
+// whole, as in the chunked kernels.
+constexpr int kOneThreads = 1024;
+constexpr int kOneSlices = 8;   // in flight
+constexpr int64_t kOneMaxReads = 65536;   // n * terms
+
+template <int KIND>
+__global__ __launch_bounds__(kOneThreads) void reduce_norm_one_kernel(SliceArgs sa, int nterms, float world,
+                                                                      float *__restrict__ out, int64_t n,
+                                                                      int accumulate, double *total, float *norm) {
+    __shared__ double lds[kOneThreads / 64];
+    const double before = accumulate ? total[0] : 0.0;
+    LaneTotal<KIND> t;
+    for (int64_t e = 4 * threadIdx.x; e < n; e += 4 * kOneThreads) {
+        float acc[4];
+        for (int t0 = 0; t0 < nterms; t0 += kOneSlices) {
+            u32x2 x[kOneSlices];
+#pragma unroll
+            for (int k = 0; k < kOneSlices; ++k)
+                if (t0 + k < nterms) x[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(sa.p[t0 + k] + e));
+#pragma unroll
+            for (int k = 0; k < kOneSlices; ++k) {
+                if (t0 + k == 0) set_bf16x4(acc, x[k]);
+                else if (t0 + k < nterms) add_bf16x4(acc, x[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = acc[k] / world;
+        if (e + 4 <= n) {
+            st16(reinterpret_cast<char *>(out + e), u4(acc));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t.add(acc[k]);
+        } else {
+            for (int k = 0; e + k < n; ++k) {
+                out[e + k] = acc[k];
+                t.add(acc[k]);
+            }
+        }
+    }
+    write_total<KIND>(norm_block_join<KIND, kOneThreads>(t, lds), before, total, norm);
 }
 
 // ------------------------------------------------- bf16 reduce dtype --
@@ -1743,6 +1832,18 @@ extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, 
         }
     }
     (void)hipGetLastError();
+    if (!skip && reduce_dtype == FS_FP32 && aligned && terms <= kTermsPerPass && n * terms <= kOneMaxReads) {
+        SliceArgs sa;
+        memset(&sa, 0, sizeof sa);
+        for (int k = 0; k < terms; ++k) sa.p[k] = slices[k];
+        if (type == FS_NORM_L2)
+            hipLaunchKernelGGL(reduce_norm_one_kernel<kL2>, dim3(1), dim3(kOneThreads), 0, stream, sa, terms,
+                               (float)world, out, n, accumulate != 0, total, norm);
+        else
+            hipLaunchKernelGGL(reduce_norm_one_kernel<kInf>, dim3(1), dim3(kOneThreads), 0, stream, sa, terms,
+                               (float)world, out, n, accumulate != 0, total, norm);
+        return check_launch(what);
+    }
     double *parts = static_cast<double *>(workspace);
     NormParts np{(int)type, parts};
     if (!skip) {

@@ -104,6 +104,17 @@ struct ClipArgs {
 
 __device__ __forceinline__ double norm_of(double total, int inf) { return inf ? total : sqrt(total); }
 
+// Thread 0 writes the total (joined to the one that stood there, where the
+// call accumulates) and the norm.
+template <int KIND>
+__device__ __forceinline__ void write_total(double t, double before, double *total, float *norm) {
+    if (threadIdx.x == 0) {
+        t = norm_join<KIND>(before, t);
+        total[0] = t;
+        if (norm) norm[0] = (float)norm_of(t, KIND == kInf);
+    }
+}
+
 // min(1, max_norm / (norm + eps)), computed in double and rounded once.  A
 // norm within the limit gives exactly 1; a NaN norm gives NaN, an infinite
 // one 0 (or 1 where max_norm is infinite too).

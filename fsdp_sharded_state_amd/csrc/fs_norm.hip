@@ -168,17 +168,6 @@ __global__ __launch_bounds__(kThreads) void norm_join_kernel(const double *__res
     if (threadIdx.x == 0) out[blockIdx.x] = t;
 }
 
-// Thread 0 writes the total (joined to the one that stood there, where the
-// call accumulates) and the norm.
-template <int KIND>
-__device__ __forceinline__ void write_total(double t, double before, double *total, float *norm) {
-    if (threadIdx.x == 0) {
-        t = norm_join<KIND>(before, t);
-        total[0] = t;
-        if (norm) norm[0] = (float)norm_of(t, KIND == kInf);
-    }
-}
-
 // Joins the partial totals in a fixed order.
 constexpr int kFinishThreads = 1024;
 
