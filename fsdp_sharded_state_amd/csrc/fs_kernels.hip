@@ -1832,7 +1832,7 @@ extern "C" int fs_reduce_shard_norm(int64_t n, int32_t world, int32_t grad_acc, 
         }
     }
     (void)hipGetLastError();
-    if (!skip && reduce_dtype == FS_FP32 && aligned && terms <= kTermsPerPass && n * terms <= kOneMaxReads) {
+    if (!skip && reduce_dtype == FS_FP32 && aligned && terms <= kTermsPerPass && n <= kOneMaxReads / terms) {
         SliceArgs sa;
         memset(&sa, 0, sizeof sa);
         for (int k = 0; k < terms; ++k) sa.p[k] = slices[k];

@@ -294,10 +294,14 @@ int64_t tiles_of(const void *p, int64_t nb, int tile) {
     return (blocks + tile - 1) / tile;
 }
 
+// Tiles of one launch: its grid counts threads in 32 bits, one thread for two
+// blocks (137 GB of tensors).
+static_assert(kNormUnroll == 2 && kClipUnroll == 2, "threads of a tile");
+int64_t max_tiles(int tile) { return UINT32_MAX / (tile / 2); }
+
 // Shared argument checks of the list calls, whose tiles are of `tile` blocks.
 int check_list(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
                const fs_dtype *dtypes, int tile, const void *total, const void *norm) {
-    int64_t tiles = 0;
     if (n_tensors < 0) return fail(FS_E_INVAL, "%s: n_tensors < 0", what);
     if (n_tensors > 0 && (!grads || !numel || !dtypes)) return fail(FS_E_INVAL, "%s: NULL list", what);
     for (int i = 0; i < n_tensors; ++i) {
@@ -309,8 +313,8 @@ int check_list(const char *what, int32_t n_tensors, const void *const *grads, co
         if (!grads[i]) return fail(FS_E_INVAL, "%s: tensor %d is NULL", what, i);
         if (misaligned(grads[i], elem_bytes(dtypes[i])))
             return fail(FS_E_ALIGN, "%s: tensor %d not aligned to its element size", what, i);
-        tiles += tiles_of(grads[i], nb, tile);
-        if (tiles > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+        if (tiles_of(grads[i], nb, tile) > max_tiles(tile))
+            return fail(FS_E_OVERFLOW, "%s: tensor %d is too large for one launch", what, i);
         if (ranges_overlap(total, 8, grads[i], nb) || (norm && ranges_overlap(norm, 4, grads[i], nb)))
             return fail(FS_E_INVAL, "%s: total or norm overlaps tensor %d", what, i);
     }
@@ -337,9 +341,9 @@ void launches_of(int32_t n_tensors, const void *const *grads, const int64_t *num
     };
     for (int i = 0; i < n_tensors; ++i) {
         if (numel[i] == 0) continue;
-        if (count == CAP) go();
-        const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
-        tiles += tiles_of(grads[i], nb, tile);
+        const int64_t nb = numel[i] * elem_bytes(dtypes[i]), t = tiles_of(grads[i], nb, tile);
+        if (count == CAP || tiles + t > max_tiles(tile)) go();
+        tiles += t;
         L.ptr[count] = static_cast<char *>(const_cast<void *>(grads[i]));
         L.size[count] = nb * 2 + (dtypes[i] == FS_FP32);
         L.tile_end[count++] = (uint32_t)tiles;
@@ -350,8 +354,6 @@ void launches_of(int32_t n_tensors, const void *const *grads, const int64_t *num
 template <class F>
 void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t *numel, const fs_dtype *dtypes, int tile,
                      F &&f) {
-    // A call of few tensors copies a short list; one whose tensors without
-    // elements bring it down to few does not.
     if (n_tensors <= kListFew)
         launches_of<kListFew>(n_tensors, grads, numel, dtypes, tile, f);
     else
@@ -460,10 +462,11 @@ extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, c
         if (numel[i] > (INT64_MAX >> 4)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large", what, i);
         if (numel[i] == 0) continue;
         const int64_t nb = numel[i] * elem_bytes(dtypes[i]);
-        tiles += tiles_of(anywhere, nb, kNormTile);
+        const int64_t t = tiles_of(anywhere, nb, kNormTile);
+        if (t > max_tiles(kNormTile)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large for one launch", what, i);
+        tiles += t;
         one_tiles = std::min<int64_t>(one_tiles + tiles_of(anywhere, nb, kOneTile), INT32_MAX);
         ++count;
-        if (tiles > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
     }
     *bytes = in_one_launch(count, one_tiles) ? 0 : norm_parts_bytes(tiles);
     return FS_OK;

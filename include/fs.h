@@ -29,7 +29,9 @@
  *     per pass of up to 32 terms, and over long buffers one per sub-range
  *     (32M elements for the reduce and the fused step, 16M for the bf16
  *     reduce dtype, 64M for AdamW), which measured faster than one launch
- *     over the whole buffer.
+ *     over the whole buffer.  The calls that give a norm end with one or two
+ *     more that join the partial totals, and a list call launches one kernel
+ *     per 192 tensors; small calls of both are a single launch.
  *   - fs_plan_info, fs_plan_param, fs_plan_segments, fs_plan_upload,
  *     fs_plan_destroy, the fs_reshard_info/upload/destroy calls and
  *     fs_last_error are infrastructure around the method's steps (reading a
@@ -40,7 +42,8 @@
  *     a CU (fewer concurrent HBM streams run faster); a kernel that another
  *     stream runs at the same time finds correspondingly less LDS on those
  *     CUs.
- *   - Inputs and outputs must not overlap, except the in-place AdamW state.
+ *   - Inputs and outputs must not overlap, except the in-place AdamW state
+ *     and the gradients that fs_clip_grads scales.
  *   - Errors are reported by return code (fs_status); the call then has
  *     launched nothing.  fs_last_error() describes the last failure of the
  *     calling thread.  No call aborts the process.
@@ -503,7 +506,8 @@ typedef struct {
  *                    that overlap in time need a workspace each.
  * Errors: FS_E_INVAL (negative counts, NULL pointers, workspace too small,
  * total, norm or workspace overlapping each other or a tensor), FS_E_DTYPE,
- * FS_E_UNSUPPORTED (another norm type), FS_E_ALIGN, FS_E_OVERFLOW, FS_E_HIP.
+ * FS_E_UNSUPPORTED (another norm type), FS_E_ALIGN, FS_E_OVERFLOW (a tensor of
+ * more than 137 GB), FS_E_HIP.
  */
 int fs_grad_norm(int32_t n_tensors, const void *const *grads, const int64_t *numel,
                  const fs_dtype *dtypes, fs_norm_type type, int32_t accumulate,

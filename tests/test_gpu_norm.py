@@ -66,6 +66,13 @@ SIZE_LISTS = {
     "spread": [1 << k for k in range(0, 20)] + [(1 << k) + 1 for k in range(0, 20)],
     "many": [3 + 37 * (i % 11) for i in range(500)],
     "large": [9_000_001, 5, 4_100_000],
+    "16_tensors": [33] * 16,
+    "17_tensors": [33] * 17,
+    "192_tensors": [5] * 192,
+    "193_tensors": [5] * 193,
+    "mostly_empty": [0 if i % 30 else 70 + i for i in range(300)],
+    "around_one_launch": [127 * 256, 200],           # 127 KB in fp32: one launch
+    "past_one_launch": [128 * 256, 130 * 256],
 }
 
 
@@ -195,7 +202,7 @@ def test_clip_special_totals(dtype):
     say("clip special", dtype)
     n = 30_011
     g = grads(n, dtype, 77)
-    g[5], g[6], g[7], g[8] = math.nan, math.inf, -math.inf, -0.0
+    g[5], g[6], g[7], g[8], g[9] = math.nan, math.inf, -math.inf, -0.0, 2.0 ** -130      # the last is subnormal
     total, norm = scalars()
     cases = [   # total, norm type, max_norm, eps, coefficient
         (0.25, 2, 1.0, 1e-6, 1.0),
@@ -491,6 +498,68 @@ def test_captured_and_replayed():
             assert float(e["norm"]) == float(c["norm"])
             for x, y in zip([e["out"], e["clip"], e["p"], *e["st"]], [c["out"], c["clip"], c["p"], *c["st"]]):
                 np.testing.assert_array_equal(bits(x), bits(y))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_lists(seed):
+    """Random counts, sizes, types, gaps and starts: total, norm and clip."""
+    rng = np.random.default_rng(seed)
+    n = int(np.exp(rng.uniform(0, np.log(400))))
+    most = np.exp(rng.uniform(0, np.log(300_000 if n > 40 else 3_000_000)))
+    sizes = [int(x) for x in np.exp(rng.uniform(0, np.log(most + 1), n)) - (rng.random(n) < 0.1)]
+    dts = [BF if rng.random() < 0.5 else F32 for _ in sizes]
+    say("random list", seed, n, int(most))
+    views, flats = packed(sizes, dts, seed=1000 * seed, gap=int(rng.integers(0, 6)), shift=int(rng.integers(0, 9)))
+    norm_type = NORMS[seed % 2]
+    gl = fs.fs_grad_list(views)
+    total, norm = scalars()
+    fs.fs_grad_norm(gl, total, norm, norm_type=norm_type)
+    ref.check_total(total, views, norm_type)
+    ref.check_norm(norm, float(total), norm_type)
+    nans = {d: int(torch.isnan(f).sum()) for d, f in flats.items()}
+    old, mx = [ref.as64(v) for v in views], 0.6 * float(norm)
+    fs.fs_clip_grads(gl, total, mx, norm_type=norm_type, norm_eps=0.0)
+    coef = ref.coef64(float(total), norm_type, mx, 0.0)
+    for v, g in zip(views, old):
+        tol = ref.CLIP_BF16 if v.dtype == BF else ref.CLIP_F32
+        assert (np.abs(ref.as64(v) - g * coef) <= tol * np.abs(g * coef) + (1e-38 if v.dtype == BF else 1e-45)).all()
+    assert nans == {d: int(torch.isnan(f).sum()) for d, f in flats.items()}
+
+
+def test_threads_share_a_list():
+    """Four host threads, each with its stream and total, one list and one set of slices."""
+    import threading
+    say("threads")
+    sizes = [70_001, 5, 400_000]
+    views, _ = packed(sizes, [F32, BF, BF], seed=4)
+    gl, sl = fs.fs_grad_list(views), fs.fs_grad_list([grads(50_000, BF, k) for k in range(8)])
+    want, want_r = scalars()[0], scalars()[0]
+    out0 = torch.empty(50_000, device="cuda")
+    fs.fs_grad_norm(gl, want)
+    fs.fs_reduce_shard_norm(sl, out0, want_r, world=8)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                t, r = torch.zeros(1, dtype=F64, device="cuda"), torch.zeros(1, dtype=F64, device="cuda")
+                out = torch.empty(50_000, device="cuda")
+                for _ in range(25):
+                    fs.fs_grad_norm(gl, t)
+                    fs.fs_reduce_shard_norm(sl, out, r, world=8)
+                    if float(t) != float(want) or float(r) != float(want_r) or not torch.equal(out, out0):
+                        bad.append(k)
+        except Exception as e:  # noqa: BLE001 -- reported below
+            bad.append((k, repr(e)))
+
+    ts = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad, bad
 
 
 def test_streams_of_their_own():

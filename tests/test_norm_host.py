@@ -54,6 +54,20 @@ def test_list_refusals(kw, code):
     assert _clip(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_clip_grads")
 
 
+@pytest.mark.parametrize("call", [_norm, _clip])
+def test_a_tensor_beyond_one_launch_is_refused(call):
+    """More than 2^32 threads' worth of one tensor; a list of that many bytes is cut."""
+    assert call(ptrs=(1 << 44,), numels=(1 << 36,)) == fs.FS_E_OVERFLOW
+    assert b"tensor 0" in fs.lib().fs_last_error()
+    assert call(ptrs=(1 << 44,), numels=(1 << 37,), codes=(0,)) == fs.FS_E_OVERFLOW
+    need = ctypes.c_int64()
+    m, c = (ctypes.c_int64 * 2)(1 << 36, 1), (ctypes.c_int32 * 2)(1, 1)
+    assert fs.lib().fs_grad_norm_workspace(2, m, c, ctypes.byref(need)) == fs.FS_E_OVERFLOW
+    m = (ctypes.c_int64 * 2)(1 << 34, 1 << 34)
+    assert fs.lib().fs_grad_norm_workspace(2, m, c, ctypes.byref(need)) == 0
+    assert need.value >= 8 * (1 << 24)     # 8 KB of gradients to a partial total
+
+
 def test_a_bad_tensor_is_named():
     assert _norm(ptrs=(GOOD, GOOD + 4096, GOOD + 8194), numels=(1, 2, 3), codes=(0, 1, 1)) == fs.FS_E_ALIGN
     assert b"tensor 2" in fs.lib().fs_last_error()
