@@ -575,11 +575,16 @@ constexpr int64_t kRedChunkFew = kWgRow * kRedGroupsFew;                // 4096 
 // terms of 25.3M elements take 275 us for 326 in chunks of 4096, of 50M 520
 // for 637, of 75.9M 801 for 850 (of 210M 2212 for 2158).  The residency cap of
 // the chunks of 4096 helps from 50M elements on (556 us without it),
-// kNormCapRounds rounds.
+// kNormCapRounds rounds.  Long passes of at most kRedFewest terms take the
+// short calls' chunks too, which read all their slices at once: 4 terms of
+// 25.3M elements 50.5 us for 52.9, of 75.9M 148 for 157 (of 4M 13.5 for 11.0).
 constexpr int kRedGroupsShort = 2, kRedSlicesShort = 4;
 constexpr int64_t kRedShort = 1 << 21;
 constexpr int64_t kRedManyMin = 1 << 27;
 constexpr int64_t kNormCapRounds = 12;
+constexpr int kRedFewest = 4;
+constexpr int64_t kRedFewestMin = 1 << 23;
+constexpr int kRedShortWgsPerCu = 8;
 
 __device__ __forceinline__ void f4(u32x4 v, float o[4]) {
     o[0] = __uint_as_float(v.x);
@@ -1423,17 +1428,19 @@ void launch_reduce_pass(int64_t n, int64_t off, int64_t len, hipStream_t stream,
     double *parts = np ? np->next : nullptr;
     int64_t grid;
     if (aligned) {
-        const bool is_short = np && n < kRedShort, few = cnt <= kRedFewTerms || (np && n < kRedManyMin);
+        const bool is_short = np && (n < kRedShort || (cnt <= kRedFewest && n >= kRedFewestMin));
+        const bool few = cnt <= kRedFewTerms || (np && n < kRedManyMin);
         const int64_t chunk = is_short ? kWgRow * kRedGroupsShort : few ? kRedChunkFew : kRedChunk;
         grid = (len + chunk - 1) / chunk;
         const dim3 g((uint32_t)grid);
-        const uint32_t lds = lds_cap(few ? kRedFewWgsPerCu : kRedManyWgsPerCu, (n + chunk - 1) / chunk,
+        const uint32_t lds = lds_cap(is_short ? kRedShortWgsPerCu : few ? kRedFewWgsPerCu : kRedManyWgsPerCu,
+                                     (n + chunk - 1) / chunk,
                                      np ? (kThreads / 64) * (int64_t)sizeof(double) : 0,
                                      np ? kNormCapRounds : kCapMinRounds);
         with_kind(np && last ? np->kind : kNoNorm, [&](auto kind) {
             constexpr int kKind = decltype(kind)::value;
             if (is_short)
-                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsShort, kRedSlicesShort>), g, dim3(kThreads), 0,
+                hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsShort, kRedSlicesShort>), g, dim3(kThreads), lds,
                                    stream, sa, cnt, first, last, world, o, len, parts);
             else if (few)
                 hipLaunchKernelGGL((reduce_chunk_kernel<kKind, kRedGroupsFew, kRedSlicesFew>), g, dim3(kThreads), lds,

@@ -260,9 +260,9 @@ def test_reduce_norm(n, N, A, shift, rd, norm_type):
     assert float(total) == (2 * before if norm_type == 2 else before)
 
 
-@pytest.mark.parametrize("n,terms", [(2_100_003, 32), (2_100_003, 40), ((1 << 21) - 1, 24), (5_000_011, 17), ((1 << 27) + 4099, 17)])
+@pytest.mark.parametrize("n,terms", [((1 << 23) + 5, 4), (2_100_003, 32), (2_100_003, 40), ((1 << 21) - 1, 24), (5_000_011, 17), ((1 << 27) + 4099, 17)])
 def test_reduce_norm_in_every_chunk_shape(n, terms):
-    """The shapes that go by length and term count; the slices are 17 to 40
+    """The shapes that go by length and term count; the slices are
     windows of one buffer, 8 elements apart."""
     say("reduce norm shapes", n, terms)
     g = torch.Generator(device="cuda").manual_seed(n)
