@@ -48,7 +48,7 @@ sys.path.insert(0, ROOT)
 
 HBM_PEAK_GBPS = 8000.0   # MI355X HBM3E peak, 8 TB/s
 KERNEL_SRCS = [os.path.join(ROOT, "fsdp_sharded_state_amd", "csrc", f)
-               for f in ("fs_kernels.hip", "fs_internal.h", "fs_plan_impl.h", "fs_plan.cpp")]
+               for f in ("fs_kernels.hip", "fs_norm.h", "fs_device.h", "fs_internal.h", "fs_plan_impl.h", "fs_plan.cpp")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_7b_shard_step.json")
 
 WORKLOADS = {
@@ -720,9 +720,10 @@ def traffic_for(kernel: str, launch_bytes_alg: float):
     return None if k is None else k.get("hbm_bytes_per_launch")
 
 
-# the reduce's kernel for passes of more than 16 terms (its template argument
-# is the number of 4-element groups per lane)
-REDUCE_KERNEL = "reduce_chunk_kernel<16>"
+# the reduce's kernel for passes of more than 16 terms (its template arguments
+# are the norm kind, none here, the number of 4-element groups per lane and
+# the slices in flight)
+REDUCE_KERNEL = "reduce_chunk_kernel<0, 16, 2>"
 
 # The library runs a call over n elements as consecutive launches over
 # sub-ranges of at most this many elements (per pass of up to 32 terms); the

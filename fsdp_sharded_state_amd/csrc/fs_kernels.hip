@@ -24,6 +24,9 @@
 //     mixed-precision section (reduce_dtype, param_dtype).
 //   re-shard and the state-dict import: "FSDP1 vs FSDP2", memory and
 //     engineering section (the shards are the sharded state dict).
+//   the reduce with norm and the clipped AdamW step (norm kinds and clip
+//     factors of the same kernels): no passage; the usual definition, as
+//     declared in fs.h.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <string.h>
