@@ -731,22 +731,25 @@ def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: 
     kind = _norm_code(norm_type)
     n, index = master.numel(), master.get_device()
     f32, bf16 = torch.float32, torch.bfloat16
-    arrays = [("master", master, (f32,)), ("exp_avg", exp_avg, (f32,)), ("exp_avg_sq", exp_avg_sq, (f32,)),
-              ("grad", grad, (f32, bf16))]
-    if param_bf16 is not None:
-        arrays.append(("param_bf16", param_bf16, (bf16,)))
-    for name, t, dtypes in arrays:
-        if t.dtype not in dtypes or t.numel() != n:
-            raise ValueError(f"fs_adamw_step_clip: {name} must be {' or '.join(map(str, dtypes))} with {n} elements")
+    gdt = bf16 if grad.dtype is bf16 else f32
+    ptrs = []
+    for name, t, dt in (("master", master, f32), ("exp_avg", exp_avg, f32), ("exp_avg_sq", exp_avg_sq, f32),
+                        ("grad", grad, gdt), ("param_bf16", param_bf16, bf16)):
+        if t is None and name == "param_bf16":
+            ptrs.append(None)
+            continue
+        if t.dtype is not dt or t.numel() != n:
+            raise ValueError(f"fs_adamw_step_clip: {name} must be {'float32 or bfloat16' if name == 'grad' else dt} "
+                             f"with {n} elements")
         if t.get_device() != index:
             raise ValueError(f"fs_adamw_step_clip: {name} is on {t.device}, master on {master.device}")
+        ptrs.append(t.data_ptr() if t.is_contiguous() else _dev_ptr(t, name))
     clip = Clip(_scalar_ptr(total, torch.float64, index, "total"), max_norm, norm_eps, kind)
-    ptrs = [_dev_ptr(t, name) if n else 0 for name, t, _ in arrays]
-    th, m, v, g = ptrs[:4]
-    p16 = ptrs[4] if param_bf16 is not None else None
+    if index < 0:
+        _dev_ptr(master, "master")      # raises
     hp = AdamWHparams(lr, beta1, beta2, eps, weight_decay, 0, int(step))
-    _launch(index, stream, lib().fs_adamw_step_clip, n, th, m, v, g,
-            FS_BF16 if grad.dtype is bf16 else FS_FP32, p16, ctypes.byref(hp), ctypes.byref(clip))
+    _launch(index, stream, lib().fs_adamw_step_clip, n, *ptrs[:4], FS_BF16 if gdt is bf16 else FS_FP32, ptrs[4],
+            ctypes.byref(hp), ctypes.byref(clip))
 
 
 def fs_copy_bytes(dst: torch.Tensor, src: torch.Tensor, stream=None):
