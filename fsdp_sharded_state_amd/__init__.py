@@ -580,24 +580,23 @@ class GradList:
 
     def __init__(self, tensors: Sequence[torch.Tensor]):
         n = len(tensors)
-        index = tensors[0].get_device() if n else None
-        ptrs, numels, codes, storages = [], [], [], {}
-        for i, t in enumerate(tensors):
-            if not t.is_cuda or not t.is_contiguous():
-                _dev_ptr(t, f"tensor {i}")      # raises
-            if t.get_device() != index:
-                raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {tensors[0].device}")
-            ptrs.append(t.data_ptr())
-            numels.append(t.numel())
-            code = _DTYPE_CODES.get(t.dtype)
-            codes.append(_dtype_code(t.dtype) if code is None else code)
-            st = t.untyped_storage()
-            at = st.data_ptr()
-            if at not in storages:
-                storages[at] = (st, at, st.nbytes())    # holding the storage keeps the memory
-        self._index: Optional[int] = index              # of their GPU; None for an empty list
+        devices = {t.get_device() for t in tensors}
+        if len(devices) > 1 or -1 in devices or not all(t.is_contiguous() for t in tensors):
+            for i, t in enumerate(tensors):
+                _dev_ptr(t, f"tensor {i}")
+                if t.device != tensors[0].device:
+                    raise ValueError(f"tensor {i} is on {t.device}, tensor 0 on {tensors[0].device}")
+        ptrs, numels = [t.data_ptr() for t in tensors], [t.numel() for t in tensors]
+        codes = [_DTYPE_CODES.get(t.dtype) for t in tensors]
+        if None in codes:
+            _dtype_code(tensors[codes.index(None)].dtype)   # raises
+        self._index: Optional[int] = devices.pop() if n else None      # of their GPU; None for an empty list
         self._same = (codes[0], numels[0]) if n and len(set(codes)) == 1 and len(set(numels)) == 1 else None
-        self._storages = list(storages.values())
+        storages = {}                                       # holding them keeps the memory
+        for t in tensors:
+            st = t.untyped_storage()
+            storages[st._cdata] = st
+        self._storages = [(st, st.data_ptr(), st.nbytes()) for st in storages.values()]
         self._n = n
         self._ptrs = (ctypes.c_void_p * max(1, n))(*ptrs)
         self._numels = (ctypes.c_int64 * max(1, n))(*numels)
