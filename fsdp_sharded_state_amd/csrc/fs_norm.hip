@@ -7,9 +7,10 @@
 // (addresses, sizes, tile counts) travels in the kernel arguments, so a call
 // copies nothing to the GPU and can be captured into a graph, and kListMax
 // tensors fit one launch.  Tensors start on any element (views of a flat
-// shard): a tile is made of the aligned 16-byte blocks that overlap the
-// tensor, and the elements of its first and last block that lie outside are
-// masked.  Such a block never crosses a page, so only mapped memory is read.
+// shard): blocks are counted from the cache line that a tensor starts in, so
+// that no two tiles share a line of it, and elements outside the tensor are
+// masked.  Loads stay inside the lines that the tensor touches, so only mapped
+// memory is read; stores write its elements only.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <string.h>
@@ -34,8 +35,10 @@ struct ListArgs {
     uint32_t tile_end[CAP];    // tiles of this tensor and those before it; UINT32_MAX past the last tensor
 };
 
+constexpr int kLine = 128;   // bytes of a cache line
+
 // A tile's place: blocks [first, first + nblk) of the tensor whose bytes are
-// [lo, hi) from the aligned address `base`.
+// [lo, hi) from the line-aligned address `base`.
 struct TileAt {
     char *base;
     int64_t first, lo, hi;
@@ -51,7 +54,7 @@ __device__ __forceinline__ TileAt tile_of(const ListArgs<CAP> &L, int a, uint32_
     const int64_t size = L.size[a];
     TileAt t;
     t.f32 = size & 1;
-    t.lo = (int64_t)(p & 15);
+    t.lo = (int64_t)(p & (kLine - 1));
     t.hi = t.lo + (size >> 1);
     t.base = reinterpret_cast<char *>(p - (uintptr_t)t.lo);
     t.first = (int64_t)(tile - before) * blocks;
@@ -74,6 +77,10 @@ __device__ __forceinline__ TileAt tile_at(const ListArgs<CAP> &L, uint32_t tile,
     }
     return tile_of<CAP>(L, a, tile, blocks);
 }
+
+// Whether block b of the tile (below its nblk) overlaps the tensor: blocks of
+// the first line may lie before it.
+__device__ __forceinline__ bool overlaps(const TileAt &t, int b) { return t.whole || 16 * (t.first + b + 1) > t.lo; }
 
 // Elements [*e_lo, *e_hi) of block b (of the tensor) lie inside the tensor.
 template <int W>
@@ -231,10 +238,13 @@ __global__ __launch_bounds__(kFinishThreads) void list_norm_one_kernel(ListArgs<
 
 // One tile per workgroup.  Over the 7B shard (3.37 GB in fp32, 1.68 in bf16)
 // and 97 odd tensors of both types, 118 MB: 128 threads with two blocks each
-// 1050 / 515 / 41.3 us, 64 threads with one block 1014 / 561 / 45.1, 256 with
-// four 1102 / 586 / 44.8; workgroups that walk several tiles 1034 to 1340,
-// residency caps 1045 to 1690.  A call whose coefficient is 1 costs its
-// workgroups' launches, 183 us over the 7B shard.
+// 1010 / 516 / 38.7 us, 64 threads with two 1016 / 521 / 39.1, 64 with one
+// 1028 / 568 / 41.8, 128 with one 1058 / 589 / 42.7; with tiles counted from
+// the tensor's first 16-byte block, which share lines, 1057 / 524 / 41.6, and
+// there 256 threads with four blocks 1102 / 586 / 44.8, workgroups that walk
+// several tiles 1034 to 1340 and residency caps 1045 to 1690 over the 7B shard
+// in fp32.  A call whose coefficient is 1 costs its workgroups' launches, 183
+// us over that shard.
 constexpr int kClipThreads = 128;
 constexpr int kClipUnroll = 2;
 constexpr int kClipTile = kClipThreads * kClipUnroll;   // 16-byte blocks of a tile (4 KB)
@@ -258,12 +268,12 @@ __device__ __forceinline__ void clip_tile(const TileAt &at, float c) {
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
         const int b = u * kClipThreads + threadIdx.x;
-        if (b < at.nblk) v[u] = ld16(at.base + 16 * (at.first + b));
+        if (b < at.nblk && overlaps(at, b)) v[u] = ld16(at.base + 16 * (at.first + b));
     }
 #pragma unroll
     for (int u = 0; u < kClipUnroll; ++u) {
         const int b = u * kClipThreads + threadIdx.x;
-        if (b >= at.nblk) continue;
+        if (b >= at.nblk || !overlaps(at, b)) continue;
         char *p = at.base + 16 * (at.first + b);
         const u32x4 x = scale_block<W>(v[u], c);
         int e_lo = 0, e_hi = 16 / W;
@@ -288,9 +298,9 @@ __global__ __launch_bounds__(kClipThreads) void list_clip_kernel(ListArgs<CAP> L
 
 int elem_bytes(fs_dtype d) { return d == FS_BF16 ? 2 : 4; }
 
-// Tiles of `tile` 16-byte blocks that cover nb > 0 bytes at p.
+// Tiles of `tile` 16-byte blocks that cover nb > 0 bytes at p and what precedes them in p's line.
 int64_t tiles_of(const void *p, int64_t nb, int tile) {
-    const int64_t blocks = ((int64_t)(reinterpret_cast<uintptr_t>(p) & 15) + nb + 15) >> 4;
+    const int64_t blocks = ((int64_t)(reinterpret_cast<uintptr_t>(p) & (kLine - 1)) + nb + 15) >> 4;
     return (blocks + tile - 1) / tile;
 }
 
@@ -361,9 +371,9 @@ void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t 
 }
 
 // Whether the norm of `count` tensors (those with elements) goes in one launch.
-// A tensor's tiles are counted as if it started on the last byte of a block,
+// A tensor's tiles are counted as if it started on the last byte of a line,
 // so that the choice and the workspace go by the sizes alone.
-const void *const anywhere = reinterpret_cast<const void *>(15);
+const void *const anywhere = reinterpret_cast<const void *>(kLine - 1);
 bool in_one_launch(int count, int64_t one_tiles) { return count <= kListMax && one_tiles <= kOneMaxTiles; }
 
 // Two tensors that share memory would be scaled twice, or raced on.
