@@ -370,11 +370,12 @@ void for_each_launch(int32_t n_tensors, const void *const *grads, const int64_t 
         launches_of<kListMax>(n_tensors, grads, numel, dtypes, tile, f);
 }
 
-// Whether the norm of `count` tensors (those with elements) goes in one launch.
-// A tensor's tiles are counted as if it started on the last byte of a line,
-// so that the choice and the workspace go by the sizes alone.
+// A norm goes in one launch where its list has at most kOneMaxTiles tiles, and
+// so no more tensors with elements than one launch takes.  A tensor's tiles
+// are counted as if it started on the last byte of a line, so that the choice
+// and the workspace go by the sizes alone.
+static_assert(kOneMaxTiles <= kListMax, "a tensor has a tile at least");
 const void *const anywhere = reinterpret_cast<const void *>(kLine - 1);
-bool in_one_launch(int count, int64_t one_tiles) { return count <= kListMax && one_tiles <= kOneMaxTiles; }
 
 // Two tensors that share memory would be scaled twice, or raced on.
 int check_disjoint(const char *what, int32_t n_tensors, const void *const *grads, const int64_t *numel,
@@ -466,7 +467,6 @@ extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, c
     if (n_tensors < 0) return fail(FS_E_INVAL, "%s: n_tensors < 0", what);
     if (n_tensors > 0 && (!numel || !dtypes)) return fail(FS_E_INVAL, "%s: NULL list", what);
     int64_t tiles = 0, one_tiles = 0;
-    int count = 0;
     for (int i = 0; i < n_tensors; ++i) {
         if (numel[i] < 0) return fail(FS_E_INVAL, "%s: tensor %d has a negative element count", what, i);
         if (numel[i] > (INT64_MAX >> 4)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large", what, i);
@@ -476,9 +476,8 @@ extern "C" int fs_grad_norm_workspace(int32_t n_tensors, const int64_t *numel, c
         if (t > max_tiles(kNormTile)) return fail(FS_E_OVERFLOW, "%s: tensor %d is too large for one launch", what, i);
         tiles += t;
         one_tiles = std::min<int64_t>(one_tiles + tiles_of(anywhere, nb, kOneTile), INT32_MAX);
-        ++count;
     }
-    *bytes = in_one_launch(count, one_tiles) ? 0 : norm_parts_bytes(tiles);
+    *bytes = one_tiles <= kOneMaxTiles ? 0 : norm_parts_bytes(tiles);
     return FS_OK;
 }
 
