@@ -559,6 +559,8 @@ def fs_reduce_adamw_step_noalloc(slices: Sequence[torch.Tensor], master: torch.T
                                               ptr(param_bf16, "param_bf16"), ctypes.byref(hp), _stream(stream)))
 
 
+_PER_THREAD_STREAM = 2   # hipStreamPerThread's handle
+
 _DTYPE_CODES = {torch.bfloat16: FS_BF16, torch.float32: FS_FP32}
 _NORM_CODES = {2: FS_NORM_L2, "2": FS_NORM_L2, math.inf: FS_NORM_INF, "inf": FS_NORM_INF}
 
@@ -646,7 +648,10 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
     """Run a launching call with GPU `index` current, on `stream` (default:
     that GPU's current stream).  scratch >= 0: that many workspace bytes and
     their count go before the stream; they belong to the stream the kernels
-    run on, so the allocator hands them out again in that stream's order."""
+    run on, so the allocator hands them out again in that stream's order.  The
+    per-thread default stream is refused there: it is a stream of its own in
+    every host thread, but has one handle, so the allocator would hand one
+    thread's workspace to another while it is in use."""
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
             return _launch(index, stream, fn, *args, scratch=scratch)
@@ -658,6 +663,8 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     if scratch < 0:
         return _check(fn(*args, handle))
+    if handle == _PER_THREAD_STREAM:
+        raise ValueError("the per-thread default stream cannot be used here: make a stream for each thread")
     if scratch == 0:
         return _check(fn(*args, None, 0, handle))
     if stream is None:
@@ -676,7 +683,9 @@ def fs_grad_norm(grads, total: torch.Tensor, norm: Optional[torch.Tensor] = None
     """Total (float64, one value: the sum of squares, or with norm_type inf
     the largest magnitude) and norm (float32, one value) of a list of bf16 and
     fp32 gradients: a sequence of tensors or a GradList.  accumulate: joined
-    to the total that stands there."""
+    to the total that stands there.  stream: a torch stream or a raw handle,
+    which is not to be destroyed before the call's work is done; not the
+    per-thread default stream."""
     kind = _norm_code(norm_type)
     gl = _grad_list(grads)
     tot = _scalar_ptr(total, torch.float64, gl._index, "total")
@@ -701,7 +710,8 @@ def fs_reduce_shard_norm(slices, out: torch.Tensor, total: torch.Tensor, norm: O
                          world: int, grad_acc: int = 1, reduce_dtype="fp32", norm_type=2.0,
                          accumulate: bool = False, stream=None):
     """fs_reduce_shard_ex (slices: a sequence or a GradList), and the total and
-    norm of the averaged gradients, as fs_grad_norm gives them for out."""
+    norm of the averaged gradients, as fs_grad_norm gives them for out.
+    stream: as there."""
     kind = _norm_code(norm_type)
     n = out.numel()
     if out.dtype is not torch.float32:
