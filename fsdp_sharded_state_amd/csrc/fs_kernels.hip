@@ -573,7 +573,11 @@ constexpr int64_t kRedChunkFew = kWgRow * kRedGroupsFew;                // 4096 
 // and its pointer in turn: in chunks of 2048 with two batches of four slices
 // in flight, 32 terms of 64K elements take 8.3 us for 30.2, of 1M 16.4 for
 // 32.8, of 2M 29.2 for 36.4 (of 4M 58.8 for 46.5; batches of eight: 7.9,
-// 16.0, 29.7, 60.6, and 4.9 for 4.3 us on 4 terms of 1K).  Up to kRedManyMin
+// 16.0, 29.7, 60.6, and 4.9 for 4.3 us on 4 terms of 1K); against chunks of
+// 4096, 4 terms of 64K elements 4.5 us for 5.1 and of 1M 5.7 for 6.9, 16 terms
+// 5.6 for 7.8 and 10.5 for 14.4.  Reduces without a norm and those of the bf16
+// reduce dtype keep their two chunk sizes at every length (32 terms of 64K
+// elements: 25.7 and 25.2 us).  Up to kRedManyMin
 // elements the chunks of 16384 make few rounds of one workgroup per CU: 32
 // terms of 25.3M elements take 275 us for 326 in chunks of 4096, of 50M 520
 // for 637, of 75.9M 801 for 850 (of 210M 2212 for 2158).  The residency cap of
@@ -786,7 +790,7 @@ constexpr int tail_groups(int g) { return g < kTailGroups ? g : kTailGroups; }
     } while (0)
 
 // KIND: kNoNorm, or (in the last pass) the norm whose partial totals, one per
-// wave, go to `parts`.
+// workgroup, go to `parts`.
 template <int KIND, int G, int SL>
 __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, int nterms, int first_pass,
                                                                 int last_pass, float world,
@@ -800,9 +804,10 @@ __global__ __launch_bounds__(kThreads) void reduce_chunk_kernel(SliceArgs sa, in
     if (KIND) store_total<KIND>(t, parts);
 }
 
-// A tiny reduce with its norm in one launch of one workgroup: the launch and
-// the workspace that it saves are worth 3 us of a caller's time.  On the GPU
-// it takes 2.4 us for 4.3 (4 terms of 1K elements), 3.5 for 4.4 (of 8K), 4.4
+// A tiny reduce with its norm in one launch of one workgroup: the launch that
+// it saves is worth 2.4 us of a caller's time (4 terms of 8K elements: 6.4 us
+// a call for 8.8).  The workspace is asked for all the same, as its size goes
+// by n alone, and stays unused.  On the GPU it takes 2.4 us for 4.3 (4 terms of 1K elements), 3.5 for 4.4 (of 8K), 4.4
 // for 6.9 (32 terms of 1K); at twice kOneMaxReads it is slower.  A lane owns
 // groups of 4 elements, 4 * kOneThreads apart; a group that n cuts is read
 // whole, as in the chunked kernels.
