@@ -17,6 +17,15 @@ ranks are processes):
 
     fs_reduce_shard_norm(slices, grad32, total, world=8, grad_acc=4)
     fs_adamw_step_clip(master, m, v, grad32, p16, total=total, max_norm=1.0, step=1)
+
+With 4-bit communication (microscaled blocks of 32):
+
+    mp = fs_mx4_plan(plan).upload()
+    fs_pack_mx4(mp, params, gathered4)    # copy-in; seed=... rounds stochastically
+    fs_unpack_mx4(mp, gathered4, outs)    # copy-out
+    fs_mx4_quantize(x, xq)                # or read a weight where it was gathered:
+    fs_mx4_matmul(xq, mp.matrix(gathered4, i), y)
+    fs_reduce_shard_mx4(mp, slices4, grad32, rank=r, grad_acc=4)
 """
 from __future__ import annotations
 
@@ -123,6 +132,21 @@ def lib() -> ctypes.CDLL:
     L.fs_reduce_shard_norm_workspace.argtypes = [i64, ctypes.POINTER(i64)]
     L.fs_adamw_step_clip.argtypes = [i64, vp, vp, vp, vp, i32, vp, ctypes.POINTER(AdamWHparams), ctypes.POINTER(Clip),
                                      vp]
+    mat = ctypes.POINTER(Mx4MatrixStruct)
+    L.fs_mx4_quantize.argtypes = [i64, i64, vp, i32, i64, mat, mat, vp, vp]
+    L.fs_mx4_dequantize.argtypes = [mat, vp, i32, i64, vp]
+    L.fs_mx4_matmul.argtypes = [mat, mat, vp, i32, i64, vp, sz, vp]
+    L.fs_mx4_matmul_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.fs_mx4_plan.argtypes = [vp, ctypes.POINTER(vp)]
+    L.fs_mx4_plan_info.argtypes = [vp, ctypes.POINTER(Mx4PlanInfo)]
+    L.fs_mx4_plan_piece.argtypes = [vp, i32, i32, ctypes.POINTER(i64), ctypes.POINTER(i64)]
+    L.fs_mx4_plan_upload.argtypes = [vp, vp, sz, vp]
+    L.fs_mx4_plan_matrix.argtypes = [vp, vp, i32, mat]
+    L.fs_mx4_plan_destroy.argtypes = [vp]
+    L.fs_mx4_plan_destroy.restype = None
+    L.fs_pack_mx4.argtypes = [vp, vp, i32, vp, i32, vp, vp]
+    L.fs_unpack_mx4.argtypes = [vp, vp, vp, i32, vp]
+    L.fs_reduce_shard_mx4.argtypes = [vp, i32, i32, vp, vp, vp]
     L.fs_copy_bytes.argtypes = [vp, vp, i64, vp]
     L.fs_stream_read.argtypes = [vp, i64, vp, vp]
     L.fs_stream_fill.argtypes = [vp, i64, ctypes.c_uint32, vp]
@@ -134,6 +158,9 @@ def lib() -> ctypes.CDLL:
                  "fs_reshard_upload", "fs_reshard", "fs_load_local", "fs_reduce_adamw_step_noalloc",
                  "fs_grad_norm", "fs_grad_norm_workspace", "fs_clip_grads", "fs_reduce_shard_norm",
                  "fs_reduce_shard_norm_workspace", "fs_adamw_step_clip",
+                 "fs_mx4_quantize", "fs_mx4_dequantize", "fs_mx4_matmul", "fs_mx4_matmul_workspace", "fs_mx4_plan",
+                 "fs_mx4_plan_info", "fs_mx4_plan_piece", "fs_mx4_plan_upload", "fs_mx4_plan_matrix", "fs_pack_mx4",
+                 "fs_unpack_mx4", "fs_reduce_shard_mx4",
                  "fs_copy_bytes", "fs_stream_read", "fs_stream_fill"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
@@ -759,6 +786,251 @@ def fs_adamw_step_clip(master: torch.Tensor, exp_avg: torch.Tensor, exp_avg_sq: 
     hp = AdamWHparams(lr, beta1, beta2, eps, weight_decay, 0, int(step))
     _launch(index, stream, lib().fs_adamw_step_clip, n, *ptrs[:4], FS_BF16 if gdt is bf16 else FS_FP32, ptrs[4],
             ctypes.byref(hp), ctypes.byref(clip))
+
+
+# ------------------------------------------------ microscaled 4-bit shards --
+
+MX4_BLOCK = 32   # elements of a block: 16 bytes of codes and one scale byte
+
+
+class Mx4MatrixStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("code_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("chunk_rows", ctypes.c_int64), ("chunk_stride", ctypes.c_int64)]
+
+
+class Mx4PlanInfo(ctypes.Structure):
+    _fields_ = [("shard_blocks", ctypes.c_int64), ("shard_bytes", ctypes.c_int64),
+                ("gathered_bytes", ctypes.c_int64), ("workspace_bytes", ctypes.c_int64)]
+
+
+def _bytes_rows(t: torch.Tensor, width: int, what: str):
+    if t.dtype is not torch.uint8 or t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{what} must be a uint8 matrix of {width} columns")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor")
+    if t.shape[1] > 1 and t.numel() and t.stride(1) != 1:
+        raise ValueError(f"{what}: the bytes of a row must follow each other")
+
+
+class Mx4Matrix:
+    """A matrix of 4-bit blocks along its rows: codes (uint8, rows by 16 for
+    each block of 32 elements) and scales (uint8, rows by one a block), each
+    with any row stride (codes: a multiple of 16 bytes).  `cols` counts
+    elements; the last block of a row may be partly filled, with zeros after
+    the last element."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, cols: int):
+        nb = -(-int(cols) // MX4_BLOCK)
+        if cols < 0:
+            raise ValueError("cols must be >= 0")
+        _bytes_rows(codes, 16 * nb, "codes")
+        _bytes_rows(scales, nb, "scales")
+        if codes.shape[0] != scales.shape[0] or codes.device != scales.device:
+            raise ValueError("codes and scales must have the same rows, on the same GPU")
+        self.codes: Optional[torch.Tensor] = codes
+        self.scales: Optional[torch.Tensor] = scales
+        self._hold(Mx4MatrixStruct(codes.data_ptr(), scales.data_ptr(), codes.shape[0], int(cols), codes.stride(0),
+                                   scales.stride(0), 0, 0), codes.get_device(), (codes, scales))
+
+    def _hold(self, m: Mx4MatrixStruct, index: int, tensors):
+        self._m, self._ref, self._index = m, ctypes.byref(m), index
+        self._tensors = [(t, t.data_ptr()) for t in tensors]
+        self.shape = (m.rows, m.cols)
+
+    @classmethod
+    def _gathered(cls, m: Mx4MatrixStruct, gathered: torch.Tensor) -> "Mx4Matrix":
+        self = cls.__new__(cls)
+        self.codes = self.scales = None     # in the gathered buffer, chunk by chunk
+        self._hold(m, gathered.get_device(), (gathered,))
+        return self
+
+    def _live(self):
+        for t, ptr in self._tensors:
+            if t.data_ptr() != ptr:
+                raise ValueError("the matrix's tensors no longer have the memory they had when it was made")
+        return self._ref
+
+
+def fs_mx4_empty(rows: int, cols: int, device="cuda") -> Mx4Matrix:
+    """Memory for a (rows, cols) matrix of 4-bit blocks, uninitialized."""
+    nb = -(-int(cols) // MX4_BLOCK)
+    return Mx4Matrix(torch.empty(rows, 16 * nb, dtype=torch.uint8, device=device),
+                     torch.empty(rows, nb, dtype=torch.uint8, device=device), cols)
+
+
+def _same_gpu(index: int, *named):
+    for name, other in named:
+        if other != index:
+            raise ValueError(f"{name} is on GPU {other}, the other arguments on cuda:{index}")
+
+
+def _plain_matrix(t: torch.Tensor, what: str) -> tuple:
+    """(address, dtype code, row stride) of a matrix whose rows are contiguous."""
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None or t.dim() != 2:
+        raise ValueError(f"{what} must be a bfloat16 or float32 matrix")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a GPU tensor")
+    rows, cols = t.shape
+    if cols > 1 and rows and t.stride(1) != 1:
+        raise ValueError(f"{what}: the elements of a row must follow each other")
+    return t.data_ptr(), code, t.stride(0)
+
+
+def fs_mx4_quantize(x: torch.Tensor, by_row: Optional[Mx4Matrix] = None, by_col: Optional[Mx4Matrix] = None, *,
+                    seed: Optional[torch.Tensor] = None, stream=None):
+    """Quantise a matrix (bf16 or fp32, any row stride) in blocks along its
+    rows into by_row, along its columns into by_col (the transpose's shape),
+    or both in one pass.  seed: None rounds to nearest; one int64 on the GPU
+    rounds stochastically by it, read when the kernel runs."""
+    ptr, code, ld = _plain_matrix(x, "x")
+    index = x.get_device()
+    rows, cols = x.shape
+    for name, m in (("by_row", by_row), ("by_col", by_col)):
+        if m is not None:
+            _same_gpu(index, (name, m._index))
+    _launch(index, stream, lib().fs_mx4_quantize, rows, cols, ptr, code, ld,
+            None if by_row is None else by_row._live(), None if by_col is None else by_col._live(),
+            _scalar_ptr(seed, torch.int64, index, "seed"))
+
+
+def fs_mx4_dequantize(m: Mx4Matrix, out: torch.Tensor, *, stream=None):
+    """The values of a matrix of 4-bit blocks, as bf16 or fp32 (out's type)."""
+    ptr, code, ld = _plain_matrix(out, "out")
+    if tuple(out.shape) != m.shape:
+        raise ValueError(f"fs_mx4_dequantize: out must be {m.shape}")
+    index = out.get_device()
+    _same_gpu(index, ("the matrix", m._index))
+    _launch(index, stream, lib().fs_mx4_dequantize, m._live(), ptr, code, ld)
+
+
+def fs_mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor, *, stream=None):
+    """out = a b^T (bf16 or fp32, any row stride): a is (m, k), b (n, k), out
+    (m, n).  Summed in fp32.  stream: a torch stream or a raw handle, which is
+    not to be destroyed before the call's work is done; not the per-thread
+    default stream."""
+    ptr, code, ld = _plain_matrix(out, "out")
+    m, k = a.shape
+    n = b.shape[0]
+    if b.shape[1] != k or tuple(out.shape) != (m, n):
+        raise ValueError(f"fs_mx4_matmul: a {a.shape} by b {b.shape} transposed does not give {tuple(out.shape)}")
+    index = out.get_device()
+    _same_gpu(index, ("a", a._index), ("b", b._index))
+    need = ctypes.c_int64()
+    _check(lib().fs_mx4_matmul_workspace(m, n, k, ctypes.byref(need)))
+    _launch(index, stream, lib().fs_mx4_matmul, a._live(), b._live(), ptr, code, ld, scratch=need.value)
+
+
+class Mx4Plan:
+    """The layout of a group's quantised shards (wraps fs_mx4_plan_t)."""
+
+    def __init__(self, plan: Plan):
+        h = ctypes.c_void_p()
+        _check(lib().fs_mx4_plan(plan._h, ctypes.byref(h)))
+        self._h = h
+        self._destroy = lib().fs_mx4_plan_destroy
+        info = Mx4PlanInfo()
+        _check(lib().fs_mx4_plan_info(h, ctypes.byref(info)))
+        self.plan = plan
+        self.shard_blocks, self.shard_bytes = info.shard_blocks, info.shard_bytes
+        self.gathered_bytes, self.workspace_bytes = info.gathered_bytes, info.workspace_bytes
+        self.workspace: Optional[torch.Tensor] = None
+
+    def close(self):
+        h = self.__dict__.pop("_h", None)
+        if h is not None and h.value:
+            self._destroy(h)
+
+    def __del__(self):
+        self.close()
+
+    def upload(self, device="cuda", stream=None) -> "Mx4Plan":
+        ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=device)
+        _launch(ws.get_device(), stream, lib().fs_mx4_plan_upload, self._h, ws.data_ptr(), ws.numel())
+        self.workspace = ws
+        return self
+
+    def piece(self, i: int, rank: int) -> tuple:
+        """(first block in the rank's shard, element count) of parameter i."""
+        b, n = ctypes.c_int64(), ctypes.c_int64()
+        _check(lib().fs_mx4_plan_piece(self._h, int(i), int(rank), ctypes.byref(b), ctypes.byref(n)))
+        return b.value, n.value
+
+    def matrix(self, gathered: torch.Tensor, i: int) -> Mx4Matrix:
+        """Parameter i where it lies in a gathered buffer (FSDP2, rows of whole blocks)."""
+        self._bytes(gathered, self.gathered_bytes, "gathered")
+        m = Mx4MatrixStruct()
+        _check(lib().fs_mx4_plan_matrix(self._h, gathered.data_ptr(), int(i), ctypes.byref(m)))
+        return Mx4Matrix._gathered(m, gathered)
+
+    @staticmethod
+    def _bytes(t: torch.Tensor, n: int, what: str) -> int:
+        if t.dtype is not torch.uint8 or t.numel() != n:
+            raise ValueError(f"{what} must be uint8 with {n} elements")
+        return _dev_ptr(t, what)
+
+    def _params(self, tensors, what: str, index: int, stream) -> tuple:
+        if not tensors:
+            return 0, FS_BF16
+        dt = tensors[0].dtype
+        for i, t in enumerate(tensors):
+            if t.dtype is not dt:
+                raise ValueError(f"{what} must share one dtype")
+            if t.get_device() != index:
+                raise ValueError(f"{what}[{i}] is on {t.device}, the buffer on cuda:{index}")
+        code = _dtype_code(dt)
+        tab = self.plan.ptr_table(tensors, what, elem_bytes=tensors[0].element_size(), stream=stream)
+        return tab.data_ptr(), code
+
+
+def fs_mx4_plan(plan: Plan) -> Mx4Plan:
+    """Lay out the quantised shards of a plan's group (fs_mx4_plan)."""
+    return Mx4Plan(plan)
+
+
+def fs_pack_mx4(mp: Mx4Plan, params: Sequence[torch.Tensor], out: torch.Tensor, rank: int = -1, *,
+                seed: Optional[torch.Tensor] = None, stream=None):
+    """All-gather copy-in in 4 bits: params (bf16 or fp32) -> out (uint8: the
+    whole gathered buffer, or rank's shard).  seed: as in fs_mx4_quantize."""
+    ptr = mp._bytes(out, mp.gathered_bytes if rank < 0 else mp.shard_bytes, "out")
+    index = out.get_device()
+    tab, code = mp._params(params, "params", index, stream)
+    _launch(index, stream, lib().fs_pack_mx4, mp._h, tab, code, ptr, int(rank),
+            _scalar_ptr(seed, torch.int64, index, "seed"))
+
+
+def fs_unpack_mx4(mp: Mx4Plan, gathered: torch.Tensor, params: Sequence[torch.Tensor], *, stream=None):
+    """All-gather copy-out of 4 bits: gathered -> params (bf16 or fp32)."""
+    ptr = mp._bytes(gathered, mp.gathered_bytes, "gathered")
+    index = gathered.get_device()
+    tab, code = mp._params(params, "params", index, stream)
+    _launch(index, stream, lib().fs_unpack_mx4, mp._h, ptr, tab, code)
+
+
+def fs_reduce_shard_mx4(mp: Mx4Plan, slices, out: torch.Tensor, *, rank: int, grad_acc: int = 1, stream=None):
+    """Average slices[j*world + k] (uint8, each rank's quantised shard; a
+    sequence, or one tensor of a row a slice) into out (fp32, shard_numel)."""
+    n, terms = mp.plan.info.shard_numel, mp.plan.info.world * int(grad_acc)
+    if out.dtype is not torch.float32 or out.numel() != n:
+        raise ValueError(f"fs_reduce_shard_mx4: out must be float32 with {n} elements")
+    if len(slices) != terms:
+        raise ValueError(f"fs_reduce_shard_mx4: need world*grad_acc = {terms} slices")
+    index, ptr = out.get_device(), _dev_ptr(out, "out")
+    if isinstance(slices, torch.Tensor):
+        if slices.dim() != 2 or slices.dtype is not torch.uint8 or slices.shape[1] != mp.shard_bytes or (
+                slices.numel() and slices.stride(1) != 1):
+            raise ValueError(f"fs_reduce_shard_mx4: slices must be uint8 rows of {mp.shard_bytes} bytes")
+        if slices.get_device() != index:
+            raise ValueError(f"fs_reduce_shard_mx4: out is on {out.device}, the slices on {slices.device}")
+        base, step = slices.data_ptr(), slices.stride(0)
+        ptrs = [base + k * step for k in range(terms)]
+    else:
+        ptrs = [mp._bytes(s, mp.shard_bytes, f"slices[{k}]") for k, s in enumerate(slices)]
+        if any(s.get_device() != index for s in slices):
+            raise ValueError(f"fs_reduce_shard_mx4: a slice is not on {out.device}")
+    _launch(index, stream, lib().fs_reduce_shard_mx4, mp._h, int(rank), int(grad_acc),
+            (ctypes.c_void_p * max(1, terms))(*ptrs), ptr)
 
 
 def fs_copy_bytes(dst: torch.Tensor, src: torch.Tensor, stream=None):

@@ -2,8 +2,9 @@
 
     python -m fsdp_sharded_state_amd.build
 
-The library is one hipcc link of the host planner (fs_plan.cpp) and the
-kernels plus launchers (fs_kernels.hip, fs_norm.hip).  Flags:
+The library is one hipcc link of the host planners (fs_plan.cpp,
+fs_mx4_plan.cpp) and the kernels plus launchers (fs_kernels.hip, fs_norm.hip,
+fs_mx4.hip, fs_mx4_matmul.hip).  Flags:
   --offload-arch=gfx950          CDNA4 only, no other targets
   -ffp-contract=off              no FMA contraction: every + and * rounds once,
                                  as the documented update formulas say
@@ -20,7 +21,8 @@ LIB = os.path.join(HERE, "libfsstate.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = [os.path.join(CSRC, "fs_plan.cpp"), os.path.join(CSRC, "fs_kernels.hip"),
-           os.path.join(CSRC, "fs_norm.hip")]
+           os.path.join(CSRC, "fs_norm.hip"), os.path.join(CSRC, "fs_mx4_plan.cpp"),
+           os.path.join(CSRC, "fs_mx4.hip"), os.path.join(CSRC, "fs_mx4_matmul.hip")]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
     "-ffp-contract=off", "-fno-fast-math",

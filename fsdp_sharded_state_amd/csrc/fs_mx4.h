@@ -1,0 +1,262 @@
+// fs_mx4.h -- the microscaled 4-bit block format as the kernels of both MX4
+// sources make and read it.  Not part of the public ABI.
+//
+// A lane works on 8 consecutive elements: 4 bytes of codes, a quarter of a
+// block.  The four lanes of a quad hold one block, so its largest magnitude
+// is joined by two quad permutes and no LDS.  CDNA4 converts a pair of values
+// to codes and back, scale and rounding included, in one instruction each
+// (checked bit for bit against the definition over every bf16 value at every
+// scale, fp32 values on and beside every midpoint, and every code at every
+// scale): 4 instructions a lane, so the conversions stay under the HBM time.
+#pragma once
+#include "fs_device.h"
+#include "fs_mx4_plan.h"
+
+namespace fsi {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// 16 bytes at any element-aligned address: the target allows unaligned
+// vector accesses, and memcpy tells the compiler that this is one.
+__device__ __forceinline__ u32x4 ld16_any(const void *p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ void st16_any(void *p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+// Eight elements of either type as they lie in memory.
+template <class T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    u32x4 v;
+};
+template <>
+struct Raw8<float> {
+    u32x4 v[2];
+};
+
+// `valid` (any value) elements from p on, zeros after them.
+__device__ __forceinline__ void load8(Raw8<uint16_t> &r, const uint16_t *p, int valid) {
+    if (valid >= 8) {
+        r.v = ld16_any(p);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = 2 * k < valid ? p[2 * k] : 0, hi = 2 * k + 1 < valid ? p[2 * k + 1] : 0;
+            w[k] = lo | (hi << 16);
+        }
+        r.v = u32x4{w[0], w[1], w[2], w[3]};
+    }
+}
+__device__ __forceinline__ void load8(Raw8<float> &r, const float *p, int valid) {
+    if (valid >= 8) {
+        r.v[0] = ld16_any(p);
+        r.v[1] = ld16_any(p + 4);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) w[k] = k < valid ? __float_as_uint(p[k]) : 0u;
+        r.v[0] = u32x4{w[0], w[1], w[2], w[3]};
+        r.v[1] = u32x4{w[4], w[5], w[6], w[7]};
+    }
+}
+
+__device__ __forceinline__ uint32_t word(const u32x4 &v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+
+// Element k as fp32.
+__device__ __forceinline__ float elem(const Raw8<uint16_t> &r, int k) {
+    const uint32_t w = word(r.v, k >> 1);
+    return __uint_as_float(k & 1 ? w & 0xFFFF0000u : w << 16);
+}
+__device__ __forceinline__ float elem(const Raw8<float> &r, int k) { return __uint_as_float(word(r.v[k >> 2], k & 3)); }
+
+// Bits of the largest magnitude as fp32: as integers they are ordered like
+// the magnitudes, with the infinity above every number and NaN above it.
+__device__ __forceinline__ uint32_t amax8(const Raw8<uint16_t> &r) {
+    u16x2 m = __builtin_bit_cast(u16x2, r.v.x & 0x7FFF7FFFu);
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, word(r.v, k) & 0x7FFF7FFFu));
+    return (uint32_t)max(m.x, m.y) << 16;
+}
+__device__ __forceinline__ uint32_t amax8(const Raw8<float> &r) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, word(r.v[k >> 2], k & 3) & 0x7FFFFFFFu);
+    return m;
+}
+
+// The largest of the quad's four values, in each of its lanes.
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, true));   // lanes 1 0 3 2
+    return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));   // lanes 2 3 0 1
+}
+
+// The scale byte of a block whose largest magnitude has these bits.
+template <bool STOCHASTIC>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+    const uint32_t e = amax >> 23;
+    if (e == 255) return 255;
+    uint32_t s = max(e, 2u) - 2;
+    if (STOCHASTIC && e >= 2 && (amax & 0x7FFFFFu) > 0x400000u) ++s;
+    return s;
+}
+// 2^(s - 127); NaN for 255.
+__device__ __forceinline__ float scale_value(uint32_t s) {
+    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
+}
+
+// (a copy first: a bit cast of a vector's element takes the vector's first)
+__device__ __forceinline__ bf16x2 bf16_pair(const u32x4 &v, int k) {
+    const uint32_t w = word(v, k);
+    return __builtin_bit_cast(bf16x2, w);
+}
+
+__device__ __forceinline__ uint32_t encode_nearest(const Raw8<uint16_t> &r, float scale) {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16_pair(r.v, 0), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16_pair(r.v, 1), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16_pair(r.v, 2), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, bf16_pair(r.v, 3), scale, 3);
+    return c;
+}
+__device__ __forceinline__ uint32_t encode_nearest(const Raw8<float> &r, float scale) {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, elem(r, 0), elem(r, 1), scale, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, elem(r, 2), elem(r, 3), scale, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, elem(r, 4), elem(r, 5), scale, 2);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, elem(r, 6), elem(r, 7), scale, 3);
+    return c;
+}
+
+struct Random8 {
+    uint32_t w[4];
+};
+
+// Philox4x32 with 7 rounds.  Seven are the fewest that pass its authors'
+// statistical tests; with 16 bits an element a call serves 8 of them.
+__device__ __forceinline__ Random8 philox8(uint64_t seed, uint64_t group, uint32_t orientation) {
+    uint32_t c0 = (uint32_t)group, c1 = (uint32_t)(group >> 32), c2 = orientation, c3 = 0;
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)p1;
+        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)p0;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return Random8{{c0, c1, c2, c3}};
+}
+
+// The code of |x| = y * 2^(s-127), y <= 6, rounded up where the fraction f of
+// the step above the code at or below y exceeds (r + 0.5) / 65536.  From 1 on
+// a step is half the value's binade: the code is the exponent and the top
+// mantissa bit, f the 22 bits under it.  Below 1 the step is 0.5.  All of it is exact.
+__device__ __forceinline__ uint32_t encode_up(float y, uint32_t r) {
+    const uint32_t b = __float_as_uint(y);
+    const bool one = b >= 0x3F800000u, half = b >= 0x3F000000u;
+    const uint32_t code = one ? (b >> 22) - (0x3F800000u >> 22) + 2 : half;
+    const float f = one ? (float)(b & 0x3FFFFFu) * 0x1p-22f : 2 * y - (half ? 1.0f : 0.0f);
+    return code + (f > fmaf((float)r, 0x1p-16f, 0x1p-17f));
+}
+template <class R>
+__device__ __forceinline__ uint32_t encode_stochastic(const R &r, uint32_t s, const Random8 &rnd) {
+    const float inv = __uint_as_float((254 - s) << 23);   // s <= 253
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t b = __float_as_uint(elem(r, k));
+        const float y = __uint_as_float(b & 0x7FFFFFFFu) * inv;
+        const uint32_t u = k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu;
+        c |= (encode_up(y, u) | (b >> 31 << 3)) << (4 * k);
+    }
+    return c;
+}
+
+// Codes and scale byte of a quad's block, from its lanes' quarters.  `group`:
+// 4 * block + the lane's quarter, for the random bits.
+template <bool STOCHASTIC, class R>
+__device__ __forceinline__ uint32_t encode8(const R &r, uint64_t seed, uint64_t group, uint32_t orientation, uint32_t *s) {
+    *s = scale_byte<STOCHASTIC>(quad_max(amax8(r)));
+    if (*s == 255) return 0;
+    if (STOCHASTIC) return encode_stochastic(r, *s, philox8(seed, group, orientation));
+    return encode_nearest(r, scale_value(*s));
+}
+
+__device__ __forceinline__ void decode8(float *v, uint32_t c, float scale) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2);
+    const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = d.x, v[5] = d.y, v[6] = e.x, v[7] = e.y;
+}
+__device__ __forceinline__ u32x4 decode8_bf16(uint32_t c, float scale) {
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3))};
+}
+
+// The first `valid` of the 8 values of codes c to p.
+__device__ __forceinline__ void store8(uint16_t *p, uint32_t c, float scale, int valid) {
+    const u32x4 v = decode8_bf16(c, scale);
+    if (valid >= 8) {
+        st16_any(p, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < valid) p[k] = (uint16_t)(word(v, k >> 1) >> (16 * (k & 1)));
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float *v, int valid) {
+    if (valid >= 8) {
+        __builtin_memcpy(p, v, 16);
+        __builtin_memcpy(p + 4, v + 4, 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < valid) p[k] = v[k];
+    }
+}
+__device__ __forceinline__ void store8(float *p, uint32_t c, float scale, int valid) {
+    float v[8];
+    decode8(v, c, scale);
+    store8(p, v, valid);
+}
+
+// A matrix of blocks, by value.
+struct Mx4Mat {
+    const uint8_t *codes, *scales;
+    int64_t code_stride, scale_stride, chunk_rows, chunk_stride;
+
+    // Byte offsets of a row's codes and scales.
+    __device__ __forceinline__ void row(int64_t r, int64_t *code, int64_t *scale) const {
+        int64_t base = 0;
+        if (chunk_rows) {
+            const int64_t c = r / chunk_rows;
+            base = c * chunk_stride;
+            r -= c * chunk_rows;
+        }
+        *code = base + r * code_stride;
+        *scale = base + r * scale_stride;
+    }
+};
+
+// ------------------------------------------------------------ host side --
+
+inline int64_t mx4_blocks(int64_t n) { return n / kMx4Block + (n % kMx4Block != 0); }
+
+// Checks a matrix argument (`m` not NULL) and gives its kernel form and the
+// bytes that its codes and scales span.
+int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, int64_t *code_span,
+                 int64_t *scale_span);
+
+}  // namespace fsi

@@ -1,0 +1,534 @@
+// fs_mx4.hip -- quantising and dequantising in blocks of 32 4-bit elements:
+// matrices, and the shards of a group (copy-in, copy-out and the reduce of
+// quantised slices).
+#include <string.h>
+
+#include "fs_mx4.h"
+
+using namespace fsi;
+
+namespace {
+
+constexpr int kQuads = kThreads / 4;                       // blocks a workgroup handles at a time
+constexpr int kTileSteps = kMx4TileBlocks / kQuads;        // a lane's quarters of a tile
+static_assert(kTileSteps * kQuads == kMx4TileBlocks, "a tile is whole steps");
+
+// ------------------------------------------------------------------ shards --
+
+template <class T, bool STOCHASTIC>
+__global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
+                                                            const Mx4Run *__restrict__ pads,
+                                                            const void *const *__restrict__ params,
+                                                            uint8_t *__restrict__ out, int32_t first_rank,
+                                                            int64_t shard_blocks, int64_t shard_bytes,
+                                                            const uint64_t *__restrict__ seed_at) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= ntiles) {   // blocks of no piece, or the bytes after the last scale
+        const Mx4Run run = pads[blockIdx.x - ntiles];
+        uint8_t *shard = out + (run.rank - first_rank) * shard_bytes;
+        if (run.n == 0) {
+            const int64_t end = shard_blocks * (kMx4BlockBytes + 1);
+            for (int64_t k = end + tid; k < shard_bytes; k += kThreads) shard[k] = 0;
+        } else if (tid < run.n) {
+            *reinterpret_cast<u32x4 *>(shard + (run.at + tid) * kMx4BlockBytes) = u32x4{0, 0, 0, 0};
+            shard[shard_blocks * kMx4BlockBytes + run.at + tid] = 0;
+        }
+        return;
+    }
+    const Mx4Tile t = tiles[blockIdx.x];
+    const T *src = static_cast<const T *>(params[t.param]) + t.src;
+    uint8_t *shard = out + (t.rank - first_rank) * shard_bytes;
+    uint32_t *codes = reinterpret_cast<uint32_t *>(shard + t.blk * kMx4BlockBytes);
+    uint8_t *scales = shard + shard_blocks * kMx4BlockBytes + t.blk;
+    const uint64_t seed = STOCHASTIC ? *seed_at : 0;
+    const uint64_t group = 4 * (uint64_t)(t.rank * shard_blocks + t.blk);
+    Raw8<T> r[kTileSteps];
+#pragma unroll
+    for (int i = 0; i < kTileSteps; ++i) {
+        const int q = i * kThreads + tid;
+        load8(r[i], src + 8 * q, t.n - 8 * q);
+    }
+#pragma unroll
+    for (int i = 0; i < kTileSteps; ++i) {
+        const int q = i * kThreads + tid;
+        uint32_t s;
+        const uint32_t c = encode8<STOCHASTIC>(r[i], seed, group + q, 0, &s);
+        if ((q >> 2) < t.nblk) {
+            codes[q] = c;
+            if ((tid & 3) == 0) scales[q >> 2] = (uint8_t)s;
+        }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void unpack_mx4_kernel(const Mx4Tile *__restrict__ tiles,
+                                                              const uint8_t *__restrict__ gathered,
+                                                              void *const *__restrict__ params, int64_t shard_blocks,
+                                                              int64_t shard_bytes) {
+    const int tid = threadIdx.x;
+    const Mx4Tile t = tiles[blockIdx.x];
+    T *dst = static_cast<T *>(params[t.param]) + t.src;
+    const uint8_t *shard = gathered + t.rank * shard_bytes;
+    const uint32_t *codes = reinterpret_cast<const uint32_t *>(shard + t.blk * kMx4BlockBytes);
+    const uint8_t *scales = shard + shard_blocks * kMx4BlockBytes + t.blk;
+    uint32_t c[kTileSteps], s[kTileSteps];
+#pragma unroll
+    for (int i = 0; i < kTileSteps; ++i) {
+        const int q = i * kThreads + tid;
+        if (8 * q < t.n) {
+            c[i] = codes[q];
+            s[i] = scales[q >> 2];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kTileSteps; ++i) {
+        const int q = i * kThreads + tid;
+        if (8 * q < t.n) store8(dst + 8 * q, c[i], scale_value(s[i]), t.n - 8 * q);
+    }
+}
+
+constexpr int kMx4Terms = 64;   // slices of one launch; the sums of more are carried through `out`
+struct Mx4Slices {
+    const uint8_t *p[kMx4Terms];
+};
+
+__global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
+                                                              const Mx4Run *__restrict__ gaps, Mx4Slices slices,
+                                                              int nterms, int first_pass, int last_pass, float world,
+                                                              float *__restrict__ out, int64_t shard_blocks) {
+    const int tid = threadIdx.x;
+    if (blockIdx.x >= ntiles) {   // elements of no piece
+        const Mx4Run run = gaps[blockIdx.x - ntiles];
+        for (int k = tid; k < run.n; k += kThreads) out[run.at + k] = 0.f;
+        return;
+    }
+    const Mx4Tile t = tiles[blockIdx.x];
+    if (tid < t.fill) out[t.elem + t.n + tid] = 0.f;
+    const int64_t code0 = t.blk * kMx4BlockBytes, scale0 = shard_blocks * kMx4BlockBytes + t.blk;
+    for (int i = 0; i < kTileSteps; ++i) {
+        const int q = i * kThreads + tid, valid = t.n - 8 * q;
+        if (valid <= 0) break;
+        float *dst = out + t.elem + 8 * q;
+        float acc[8];
+        if (!first_pass) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = k < valid ? dst[k] : 0.f;
+        }
+        for (int j = 0; j < nterms; ++j) {
+            const uint32_t c = *reinterpret_cast<const uint32_t *>(slices.p[j] + code0 + 4 * q);
+            float v[8];
+            decode8(v, c, scale_value(slices.p[j][scale0 + (q >> 2)]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = j == 0 && first_pass ? v[k] : acc[k] + v[k];
+        }
+        if (last_pass) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[k] = acc[k] / world;
+        }
+        store8(dst, acc, valid);
+    }
+}
+
+// ---------------------------------------------------------------- matrices --
+
+constexpr int kMatTile = 128;                                  // rows and columns of a tile
+constexpr int kMatQuarters = kMatTile / 8;                     // lanes' quarters along it
+constexpr int kMatSteps = kMatTile * kMatQuarters / kThreads;
+
+struct Mx4Out {
+    uint8_t *codes, *scales;
+    int64_t code_stride, scale_stride;
+};
+
+// One tile: its rows' blocks straight from the loads, its columns' from a copy in LDS.
+template <class T, bool ROWS, bool COLS, bool STOCHASTIC>
+__global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
+                                                                int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
+                                                                Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
+    constexpr int kPitch = kMatTile + 2;
+    __shared__ T lds[COLS ? kMatTile * kPitch : 1];
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kMatTile, c0 = (int64_t)(blockIdx.x % tiles_x) * kMatTile;
+    const uint64_t seed = STOCHASTIC ? *seed_at : 0;
+    const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
+#pragma unroll
+    for (int i = 0; i < kMatSteps; ++i) {
+        const int q = i * kThreads + threadIdx.x, lr = q / kMatQuarters, lq = q % kMatQuarters;
+        const int64_t r = r0 + lr, c = c0 + 8 * lq;
+        Raw8<T> v;
+        load8(v, x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
+        if (ROWS) {
+            const int64_t b = c / kMx4Block;
+            uint32_t s;
+            const uint32_t code = encode8<STOCHASTIC>(v, seed, 4 * (uint64_t)(r * nbr + b) + (lq & 3), 0, &s);
+            if (r < rows && b < nbr) {
+                *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
+                if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
+            }
+        }
+        if (COLS) {
+            T e[8];
+            __builtin_memcpy(e, &v, sizeof e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) lds[lr * kPitch + 8 * lq + k] = e[k];
+        }
+    }
+    if (!COLS) return;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMatSteps; ++i) {
+        const int q = i * kThreads + threadIdx.x, lc = q / kMatQuarters, lq = q % kMatQuarters;
+        const int64_t c = c0 + lc, b = r0 / kMx4Block + lq / 4;
+        T e[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) e[k] = lds[(8 * lq + k) * kPitch + lc];
+        Raw8<T> v;
+        __builtin_memcpy(&v, e, sizeof v);
+        uint32_t s;
+        const uint32_t code = encode8<STOCHASTIC>(v, seed, 4 * (uint64_t)(c * nbc + b) + (lq & 3), 1, &s);
+        if (c < cols && b < nbc) {
+            *reinterpret_cast<uint32_t *>(by_col.codes + c * by_col.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
+            if ((lq & 3) == 0) by_col.scales[c * by_col.scale_stride + b] = (uint8_t)s;
+        }
+    }
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
+                                                                  int64_t ldo, uint32_t tiles_x) {
+    const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kMatTile, c0 = (int64_t)(blockIdx.x % tiles_x) * kMatTile;
+#pragma unroll
+    for (int i = 0; i < kMatSteps; ++i) {
+        const int q = i * kThreads + threadIdx.x;
+        const int64_t r = r0 + q / kMatQuarters, c = c0 + 8 * (q % kMatQuarters);
+        if (r >= rows || c >= cols) continue;
+        int64_t code, scale;
+        m.row(r, &code, &scale);
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
+        store8(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
+    }
+}
+
+// ---------------------------------------------------------------- launching --
+
+int current_device(const char *what, int *dev) {
+    if (hipGetDevice(dev) != hipSuccess) return fail(FS_E_HIP, "%s: no current device", what);
+    return FS_OK;
+}
+
+// The tables live on the device they were uploaded to.
+int check_plan(const char *what, fs_mx4_plan_t p) {
+    if (!p) return fail(FS_E_INVAL, "%s: plan is NULL", what);
+    if (!p->dev_ws) return fail(FS_E_INVAL, "%s: plan has no uploaded workspace (call fs_mx4_plan_upload)", what);
+    int dev = -1;
+    if (int rc = current_device(what, &dev)) return rc;
+    if (dev != p->dev_id)
+        return fail(FS_E_INVAL, "%s: the plan was uploaded on device %d, current device is %d", what, p->dev_id, dev);
+    return FS_OK;
+}
+
+int check_dtype(const char *what, fs_dtype dtype) {
+    if (dtype != FS_BF16 && dtype != FS_FP32) return fail(FS_E_DTYPE, "%s: unknown dtype %d", what, (int)dtype);
+    return FS_OK;
+}
+int64_t width(fs_dtype dtype) { return dtype == FS_BF16 ? 2 : 4; }
+
+// A grid's threads are counted in 32 bits.
+constexpr int64_t kMaxGrid = UINT32_MAX / kThreads;
+
+const Mx4Tile *tiles_at(fs_mx4_plan_t p, int32_t rank) {
+    return reinterpret_cast<const Mx4Tile *>(static_cast<const char *>(p->dev_ws) + p->ws_tiles) + p->tile_off[rank];
+}
+const Mx4Run *pads_at(fs_mx4_plan_t p, int32_t rank) {
+    return reinterpret_cast<const Mx4Run *>(static_cast<const char *>(p->dev_ws) + p->ws_pads) + p->pad_off[rank];
+}
+const Mx4Run *gaps_at(fs_mx4_plan_t p, int32_t rank) {
+    return reinterpret_cast<const Mx4Run *>(static_cast<const char *>(p->dev_ws) + p->ws_gaps) + p->gap_off[rank];
+}
+
+// f(T value, std::bool_constant) by the element type and whether there is a seed.
+template <class F>
+void by_type(fs_dtype dtype, bool stochastic, F &&f) {
+    if (dtype == FS_BF16) {
+        if (stochastic) f(uint16_t{}, std::true_type{});
+        else f(uint16_t{}, std::false_type{});
+    } else {
+        if (stochastic) f(float{}, std::true_type{});
+        else f(float{}, std::false_type{});
+    }
+}
+
+int check_seed(const char *what, const uint64_t *seed) {
+    if (misaligned(seed, 8)) return fail(FS_E_ALIGN, "%s: seed not 8-byte aligned", what);
+    return FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_mx4_plan_upload(fs_mx4_plan_t p, void *workspace, size_t bytes, hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_mx4_plan_upload";
+    if (!p || !workspace) return fail(FS_E_INVAL, "%s: NULL argument", what);
+    if (misaligned(workspace, 16)) return fail(FS_E_ALIGN, "%s: workspace must be 16-byte aligned", what);
+    if ((int64_t)bytes < p->info.workspace_bytes)
+        return fail(FS_E_INVAL, "%s: workspace too small (%zu < %lld bytes)", what, bytes, (long long)p->info.workspace_bytes);
+    int dev = -1;
+    if (int rc = current_device(what, &dev)) return rc;
+    hipPointerAttribute_t a;
+    memset(&a, 0, sizeof a);
+    const hipError_t known = hipPointerGetAttributes(&a, workspace);
+    if (known != hipSuccess) (void)hipGetLastError();   // the query's error is not a launch error
+    if (known != hipSuccess || a.type != hipMemoryTypeDevice || a.device != dev)
+        return fail(FS_E_INVAL, "%s: workspace must be device memory of the current device (%d)", what, dev);
+    char *ws = static_cast<char *>(workspace);
+    struct Part { int64_t off; const void *src; size_t bytes; };
+    const Part parts[] = {{p->ws_tiles, p->tiles.data(), p->tiles.size() * sizeof(Mx4Tile)},
+                          {p->ws_pads, p->pads.data(), p->pads.size() * sizeof(Mx4Run)},
+                          {p->ws_gaps, p->gaps.data(), p->gaps.size() * sizeof(Mx4Run)}};
+    for (const Part &part : parts) {
+        if (part.bytes == 0) continue;
+        const hipError_t e = hipMemcpyAsync(ws + part.off, part.src, part.bytes, hipMemcpyHostToDevice, stream);
+        if (e != hipSuccess) return fail(FS_E_HIP, "%s: copy failed: %s", what, hipGetErrorString(e));
+    }
+    const hipError_t e = hipStreamSynchronize(stream);
+    if (e != hipSuccess) return fail(FS_E_HIP, "%s: sync failed: %s", what, hipGetErrorString(e));
+    p->dev_ws = workspace;
+    p->dev_id = dev;
+    return FS_OK;
+}
+
+extern "C" int fs_pack_mx4(fs_mx4_plan_t p, const void *const *params, fs_dtype param_dtype, void *out, int32_t rank,
+                           const uint64_t *seed, hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_pack_mx4";
+    if (int rc = check_plan(what, p)) return rc;
+    if (int rc = check_dtype(what, param_dtype)) return rc;
+    if (rank < -1 || rank >= p->world) return fail(FS_E_INVAL, "%s: rank %d out of range [-1, %d)", what, rank, p->world);
+    if (int rc = check_seed(what, seed)) return rc;
+    const int32_t lo = rank < 0 ? 0 : rank, hi = rank < 0 ? p->world : rank + 1;
+    const int64_t ntiles = p->tile_off[hi] - p->tile_off[lo], npads = p->pad_off[hi] - p->pad_off[lo];
+    if (ntiles + npads == 0) return FS_OK;
+    if (!out) return fail(FS_E_INVAL, "%s: out is NULL", what);
+    if (!params) return fail(FS_E_INVAL, "%s: params is NULL", what);
+    if (misaligned(out, 16)) return fail(FS_E_ALIGN, "%s: out not 16-byte aligned", what);
+    if (seed && ranges_overlap(seed, 8, out, (hi - lo) * p->info.shard_bytes))
+        return fail(FS_E_INVAL, "%s: seed inside out", what);
+    if (ntiles + npads > kMaxGrid) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+    (void)hipGetLastError();
+    by_type(param_dtype, seed != nullptr, [&](auto t, auto stochastic) {
+        hipLaunchKernelGGL((pack_mx4_kernel<decltype(t), decltype(stochastic)::value>), dim3((uint32_t)(ntiles + npads)),
+                           dim3(kThreads), 0, stream, tiles_at(p, lo), (uint32_t)ntiles, pads_at(p, lo), params,
+                           static_cast<uint8_t *>(out), lo, p->info.shard_blocks, p->info.shard_bytes, seed);
+    });
+    return check_launch(what);
+}
+
+extern "C" int fs_unpack_mx4(fs_mx4_plan_t p, const void *gathered, void *const *params, fs_dtype param_dtype,
+                             hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_unpack_mx4";
+    if (int rc = check_plan(what, p)) return rc;
+    if (int rc = check_dtype(what, param_dtype)) return rc;
+    const int64_t ntiles = (int64_t)p->tiles.size();
+    if (ntiles == 0) return FS_OK;
+    if (!gathered) return fail(FS_E_INVAL, "%s: gathered is NULL", what);
+    if (!params) return fail(FS_E_INVAL, "%s: params is NULL", what);
+    if (misaligned(gathered, 16)) return fail(FS_E_ALIGN, "%s: gathered not 16-byte aligned", what);
+    if (ntiles > kMaxGrid) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+    (void)hipGetLastError();
+    by_type(param_dtype, false, [&](auto t, auto) {
+        hipLaunchKernelGGL((unpack_mx4_kernel<decltype(t)>), dim3((uint32_t)ntiles), dim3(kThreads), 0, stream,
+                           tiles_at(p, 0), static_cast<const uint8_t *>(gathered), params, p->info.shard_blocks,
+                           p->info.shard_bytes);
+    });
+    return check_launch(what);
+}
+
+extern "C" int fs_reduce_shard_mx4(fs_mx4_plan_t p, int32_t rank, int32_t grad_acc, const void *const *slices, float *out,
+                                   hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_reduce_shard_mx4";
+    if (int rc = check_plan(what, p)) return rc;
+    if (rank < 0 || rank >= p->world) return fail(FS_E_INVAL, "%s: rank %d out of range [0, %d)", what, rank, p->world);
+    if (grad_acc < 1) return fail(FS_E_INVAL, "%s: grad_acc must be >= 1", what);
+    if (p->shard_numel == 0) return FS_OK;
+    if (!out || !slices) return fail(FS_E_INVAL, "%s: NULL argument", what);
+    if (misaligned(out, 4)) return fail(FS_E_ALIGN, "%s: out not aligned to 4 bytes", what);
+    const int64_t terms = (int64_t)p->world * grad_acc;
+    if (terms > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many slices", what);
+    for (int64_t k = 0; k < terms; ++k) {
+        if (!slices[k]) return fail(FS_E_INVAL, "%s: slice %lld is NULL", what, (long long)k);
+        if (misaligned(slices[k], 16)) return fail(FS_E_ALIGN, "%s: slice %lld not 16-byte aligned", what, (long long)k);
+        if (ranges_overlap(slices[k], p->info.shard_bytes, out, p->shard_numel * 4))
+            return fail(FS_E_INVAL, "%s: out overlaps slice %lld", what, (long long)k);
+    }
+    const int64_t ntiles = p->tile_off[rank + 1] - p->tile_off[rank], ngaps = p->gap_off[rank + 1] - p->gap_off[rank];
+    if (ntiles + ngaps > kMaxGrid) return fail(FS_E_OVERFLOW, "%s: too many tiles for one launch", what);
+    (void)hipGetLastError();
+    for (int64_t k = 0; k < terms; k += kMx4Terms) {
+        Mx4Slices s;
+        memset(&s, 0, sizeof s);
+        const int count = (int)imin(kMx4Terms, terms - k);
+        for (int j = 0; j < count; ++j) s.p[j] = static_cast<const uint8_t *>(slices[k + j]);
+        hipLaunchKernelGGL(reduce_mx4_kernel, dim3((uint32_t)(ntiles + ngaps)), dim3(kThreads), 0, stream,
+                           tiles_at(p, rank), (uint32_t)ntiles, gaps_at(p, rank), s, count, k == 0, k + count == terms,
+                           (float)p->world, out, p->info.shard_blocks);
+    }
+    return check_launch(what);
+}
+
+namespace fsi {
+
+int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, int64_t *code_span,
+                 int64_t *scale_span) {
+    constexpr int64_t kMost = (int64_t)1 << 56;   // sums of these stay within int64
+    *code_span = *scale_span = 0;
+    memset(out, 0, sizeof *out);
+    if (m->rows < 0 || m->cols < 0) return fail(FS_E_INVAL, "%s: %s has a negative size", what, name);
+    if (m->rows > INT32_MAX || m->cols > INT32_MAX)
+        return fail(FS_E_OVERFLOW, "%s: %s has more than 2^31 - 1 rows or columns", what, name);
+    if (m->rows == 0 || m->cols == 0) return FS_OK;
+    const int64_t nb = mx4_blocks(m->cols);
+    if (!m->codes || !m->scales) return fail(FS_E_INVAL, "%s: %s is NULL", what, name);
+    if (m->chunk_rows < 0) return fail(FS_E_INVAL, "%s: %s has negative chunk_rows", what, name);
+    const int64_t run = m->chunk_rows ? imin(m->chunk_rows, m->rows) : m->rows;   // rows of a chunk
+    if ((run > 1 && (m->code_stride < nb * kMx4BlockBytes || m->scale_stride < nb)))
+        return fail(FS_E_INVAL, "%s: the rows of %s overlap", what, name);
+    if (misaligned(m->codes, 16) || (m->code_stride & 15) || (m->chunk_rows && (m->chunk_stride & 15)))
+        return fail(FS_E_ALIGN, "%s: the codes of %s are not on 16 bytes", what, name);
+    const int64_t chunks = m->chunk_rows ? (m->rows + m->chunk_rows - 1) / m->chunk_rows : 1;
+    if (m->code_stride > kMost / run || m->scale_stride > kMost / run || (chunks > 1 && m->chunk_stride > kMost / chunks))
+        return fail(FS_E_OVERFLOW, "%s: the strides of %s are too large", what, name);
+    const int64_t codes = (run - 1) * m->code_stride + nb * kMx4BlockBytes, scales = (run - 1) * m->scale_stride + nb;
+    // the chunks' codes (or scales) follow each other; the two may lie between each other, as in a gathered buffer
+    if (chunks > 1 && (m->chunk_stride < codes || m->chunk_stride < scales))
+        return fail(FS_E_INVAL, "%s: the chunks of %s overlap", what, name);
+    const int64_t far = chunks > 1 ? (chunks - 1) * m->chunk_stride : 0;
+    *code_span = far + codes;
+    *scale_span = far + scales;
+    out->codes = static_cast<const uint8_t *>(m->codes);
+    out->scales = static_cast<const uint8_t *>(m->scales);
+    out->code_stride = run > 1 ? m->code_stride : 0;
+    out->scale_stride = run > 1 ? m->scale_stride : 0;
+    out->chunk_rows = chunks > 1 ? m->chunk_rows : 0;
+    out->chunk_stride = chunks > 1 ? m->chunk_stride : 0;
+    return FS_OK;
+}
+
+}  // namespace fsi
+
+namespace {
+
+struct Span {
+    const void *p;
+    int64_t bytes;
+    const char *name;
+};
+
+// Output matrix `m` of `rows` by `cols`; its codes and scales are appended to the spans, which must be disjoint of them.
+int check_out(const char *what, const char *name, const fs_mx4_matrix_t *m, int64_t rows, int64_t cols, Mx4Out *out,
+              Span *spans, int *count) {
+    Mx4Mat k;
+    int64_t code_span, scale_span;
+    if (m->rows != rows || m->cols != cols)
+        return fail(FS_E_INVAL, "%s: %s must be %lld by %lld", what, name, (long long)rows, (long long)cols);
+    if (m->chunk_rows != 0) return fail(FS_E_INVAL, "%s: %s is chunked", what, name);
+    if (int rc = check_matrix(what, name, m, &k, &code_span, &scale_span)) return rc;
+    const Span mine[] = {{k.codes, code_span, name}, {k.scales, scale_span, name}};
+    for (const Span &s : mine) {
+        for (int i = 0; i < *count; ++i)
+            if (ranges_overlap(s.p, s.bytes, spans[i].p, spans[i].bytes))
+                return fail(FS_E_INVAL, "%s: %s overlaps %s", what, name, spans[i].name);
+        spans[(*count)++] = s;
+    }
+    *out = Mx4Out{const_cast<uint8_t *>(k.codes), const_cast<uint8_t *>(k.scales), k.code_stride, k.scale_stride};
+    return FS_OK;
+}
+
+// Checks a plain matrix of `width` bytes an element and gives the bytes it spans.
+int check_plain(const char *what, const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t width,
+                int64_t *span) {
+    *span = 0;
+    if (rows < 0 || cols < 0) return fail(FS_E_INVAL, "%s: negative size", what);
+    if (rows > INT32_MAX || cols > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: more than 2^31 - 1 rows or columns", what);
+    if (rows == 0 || cols == 0) return FS_OK;
+    if (!p) return fail(FS_E_INVAL, "%s: %s is NULL", what, name);
+    if (misaligned(p, width)) return fail(FS_E_ALIGN, "%s: %s not aligned to its element size", what, name);
+    if (rows > 1 && ld < cols) return fail(FS_E_INVAL, "%s: the rows of %s overlap", what, name);
+    if (rows > 1 && ld > ((int64_t)1 << 56) / rows) return fail(FS_E_OVERFLOW, "%s: %s is too large", what, name);
+    *span = ((rows > 1 ? (rows - 1) * ld : 0) + cols) * width;
+    return FS_OK;
+}
+
+int mat_tiles(const char *what, int64_t rows, int64_t cols, uint32_t *across, uint32_t *tiles) {
+    const int64_t x = (cols + kMatTile - 1) / kMatTile, y = (rows + kMatTile - 1) / kMatTile;
+    if (x * y > kMaxGrid) return fail(FS_E_OVERFLOW, "%s: too large for one launch", what);
+    *across = (uint32_t)x;
+    *tiles = (uint32_t)(x * y);
+    return FS_OK;
+}
+
+}  // namespace
+
+extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dtype dtype, int64_t ldx,
+                               const fs_mx4_matrix_t *by_row, const fs_mx4_matrix_t *by_col, const uint64_t *seed,
+                               hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_mx4_quantize";
+    if (int rc = check_dtype(what, dtype)) return rc;
+    if (!by_row && !by_col) return fail(FS_E_INVAL, "%s: no output", what);
+    if (int rc = check_seed(what, seed)) return rc;
+    Span spans[6];
+    int count = 0;
+    int64_t span;
+    if (int rc = check_plain(what, "x", x, rows, cols, ldx, width(dtype), &span)) return rc;
+    spans[count++] = Span{x, span, "x"};
+    spans[count++] = Span{seed, seed ? 8 : 0, "seed"};
+    Mx4Out row{}, col{};
+    if (by_row)
+        if (int rc = check_out(what, "by_row", by_row, rows, cols, &row, spans, &count)) return rc;
+    if (by_col)
+        if (int rc = check_out(what, "by_col", by_col, cols, rows, &col, spans, &count)) return rc;
+    uint32_t across, tiles;
+    if (int rc = mat_tiles(what, rows, cols, &across, &tiles)) return rc;
+    if (tiles == 0) return FS_OK;
+    (void)hipGetLastError();
+    by_type(dtype, seed != nullptr, [&](auto t, auto stochastic) {
+        using T = decltype(t);
+        constexpr bool S = decltype(stochastic)::value;
+        const T *src = static_cast<const T *>(x);
+        const int64_t ld = rows > 1 ? ldx : 0;
+        if (by_row && by_col)
+            hipLaunchKernelGGL((quantize_mx4_kernel<T, true, true, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
+                               cols, src, ld, across, row, col, seed);
+        else if (by_row)
+            hipLaunchKernelGGL((quantize_mx4_kernel<T, true, false, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
+                               cols, src, ld, across, row, col, seed);
+        else
+            hipLaunchKernelGGL((quantize_mx4_kernel<T, false, true, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
+                               cols, src, ld, across, row, col, seed);
+    });
+    return check_launch(what);
+}
+
+extern "C" int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype dtype, int64_t ldo, hipStream_t stream) {
+    clear_error();
+    const char *what = "fs_mx4_dequantize";
+    if (!m) return fail(FS_E_INVAL, "%s: the matrix is NULL", what);
+    if (int rc = check_dtype(what, dtype)) return rc;
+    Mx4Mat k;
+    int64_t code_span, scale_span, span;
+    if (int rc = check_matrix(what, "the matrix", m, &k, &code_span, &scale_span)) return rc;
+    if (int rc = check_plain(what, "out", out, m->rows, m->cols, ldo, width(dtype), &span)) return rc;
+    if (ranges_overlap(out, span, k.codes, code_span) || ranges_overlap(out, span, k.scales, scale_span))
+        return fail(FS_E_INVAL, "%s: out overlaps the matrix", what);
+    uint32_t across, tiles;
+    if (int rc = mat_tiles(what, m->rows, m->cols, &across, &tiles)) return rc;
+    if (tiles == 0) return FS_OK;
+    (void)hipGetLastError();
+    by_type(dtype, false, [&](auto t, auto) {
+        using T = decltype(t);
+        hipLaunchKernelGGL(dequantize_mx4_kernel<T>, dim3(tiles), dim3(kThreads), 0, stream, k, m->rows, m->cols,
+                           static_cast<T *>(out), m->rows > 1 ? ldo : 0, across);
+    });
+    return check_launch(what);
+}

@@ -572,6 +572,206 @@ int fs_adamw_step_clip(int64_t n, float *master, float *exp_avg, float *exp_avg_
                        const fs_adamw_hparams_t *hp, const fs_clip_t *clip,
                        hipStream_t stream);
 
+/* ------------------------------------------------ microscaled 4-bit shards --
+ *
+ * Parameters and gradients that cross the links in 4.25 bits an element: the
+ * all-gather copy-in that quantises, the copy-out that dequantises, the
+ * reduce of quantised gradient slices, and the product that reads a quantised
+ * weight where the all-gather left it.  The pages do not define these; the
+ * element and scale formats are those of the OCP Microscaling Formats (MX)
+ * specification v1.0 (MXFP4: e2m1 elements, one e8m0 scale for 32).
+ *
+ * A block is 32 consecutive elements: 16 bytes of codes, the first element in
+ * the low half of the first byte, each code a sign bit over the index of its
+ * magnitude in {0, 0.5, 1, 1.5, 2, 3, 4, 6}; and one scale byte s, which
+ * multiplies them by 2^(s-127).  s = 255 makes all 32 elements NaN.
+ *
+ * Quantising a block: let amax be its largest magnitude, amax = a * 2^E with
+ * 1 <= a < 2.
+ *   nearest (seed NULL): s = max(E - 2, -127) + 127; each element / 2^(s-127)
+ *       is rounded to the nearest code, ties to the even index, and what lies
+ *       above 6 becomes 6.
+ *   stochastic (seed given): s is one more where a > 1.5 (and E - 2 >= -127),
+ *       so that nothing lies above 6 and the result's expectation is the
+ *       element to within 2^-17 of a step; an element that lies the fraction
+ *       f of the way from one code to the next goes up where
+ *       f > (r + 0.5) / 65536.  r: 16 bits of Philox4x32 (Salmon et al.,
+ *       "Parallel random numbers: as easy as 1, 2, 3", 2011) with 7 rounds,
+ *       key = the seed's low and high 32 bits, counter = (low and high 32
+ *       bits of 4*block + g, orientation, 0) for elements 8g to 8g+7 of a
+ *       block: element 8g+j takes half j%2 (0: the low one) of output word
+ *       j/2.  Nothing is stored; the same seed gives the same codes.
+ * Signs are kept, also of zeros.  A block that holds an infinity or a NaN gets
+ * s = 255 and codes of zero.  The elements that fill up a last block are +0.
+ */
+
+/* A matrix of blocks along its rows: `rows` rows of `cols` elements, each
+ * ceil(cols/32) blocks.  Row r's codes start at codes + r * code_stride bytes,
+ * its scales at scales + r * scale_stride.  With chunk_rows > 0 the rows lie
+ * in chunks of that many, chunk_stride bytes apart (in codes and in scales
+ * alike), and the strides count within a chunk.  codes, code_stride and
+ * chunk_stride are multiples of 16. */
+typedef struct {
+    void *codes;
+    void *scales;
+    int64_t rows;
+    int64_t cols;
+    int64_t code_stride;
+    int64_t scale_stride;
+    int64_t chunk_rows;    /* 0: the rows are one run */
+    int64_t chunk_stride;
+} fs_mx4_matrix_t;
+
+/*
+ * fs_mx4_quantize -- quantise a matrix along its rows, its columns, or both
+ * in one pass (a layer's products contract over different dimensions).
+ *
+ *   rows, cols      >= 0.
+ *   x      (device) row r starts at x + r * ldx elements; ldx >= cols.
+ *   dtype           of x: FS_BF16 or FS_FP32.
+ *   by_row (host)   NULL, or a (rows, cols) matrix to be written: blocks along
+ *                   x's rows.  Block b of row r has index r * ceil(cols/32) + b
+ *                   in the random counter, orientation 0.
+ *   by_col (host)   NULL, or a (cols, rows) matrix: the transpose, blocks along
+ *                   x's columns; orientation 1.
+ *   seed   (device) NULL: nearest; else one 64-bit value: stochastic.  It is
+ *                   read when the kernel runs, so a captured call takes the
+ *                   value that stands there at each replay.
+ * Only the codes and scales of the two matrices' blocks are written, nothing
+ * between their rows.
+ * Errors: FS_E_INVAL (negative sizes, NULL pointers, both outputs NULL, wrong
+ * sizes or strides, a chunked output, outputs that overlap x, the seed or each
+ * other), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW (too large for one launch),
+ * FS_E_HIP.
+ */
+int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dtype dtype, int64_t ldx,
+                    const fs_mx4_matrix_t *by_row, const fs_mx4_matrix_t *by_col,
+                    const uint64_t *seed, hipStream_t stream);
+
+/*
+ * fs_mx4_dequantize -- the values of a quantised matrix.
+ *
+ *   m     (host)    the matrix; chunked ones too.
+ *   out   (device)  element (r, c) at out + r * ldo + c; ldo >= cols.
+ *   dtype           of out: FS_FP32 (exact, overflow to infinity aside) or
+ *                   FS_BF16 (exact too, but for the nearest-even rounding of
+ *                   values below bf16's normal range).
+ * Errors: as fs_mx4_quantize.
+ */
+int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype dtype, int64_t ldo,
+                      hipStream_t stream);
+
+/*
+ * fs_mx4_matmul -- out = a * b^T: out[i][j] = sum over k of a[i][k] * b[j][k].
+ *
+ *   a, b  (host)    matrices with the same cols, each maybe chunked (a weight
+ *                   in the gathered buffer: fs_mx4_plan_matrix).
+ *   out   (device)  a->rows by b->rows elements of `dtype`, row i at
+ *                   out + i * ldo; ldo >= b->rows.  Products are exact and
+ *                   summed in fp32; a bf16 output is rounded once.  With cols
+ *                   = 0 the output is zero.
+ *   dtype           FS_BF16 or FS_FP32.
+ *   workspace (device) fs_mx4_matmul_workspace bytes, 16-byte aligned; may hold
+ *                   anything, and is in use until the call's work is done, so
+ *                   calls that may overlap in time need one each.
+ * The order of the sums depends on the sizes alone, so results are
+ * reproducible.  A linear layer y = x W^T and its gradients dx = dy W and
+ * dW = dy^T x are three such products: of x and W by row, of dy by row and W
+ * by column, of dy and x by column.
+ * Errors: FS_E_INVAL (NULL pointers, different cols, strides too small, a
+ * workspace too small or overlapping), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW,
+ * FS_E_HIP.
+ */
+int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b, void *out, fs_dtype dtype,
+                  int64_t ldo, void *workspace, size_t bytes, hipStream_t stream);
+
+/* fs_mx4_matmul_workspace -- workspace bytes (may be 0) of an m by n product
+ * over k elements. */
+int fs_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t *bytes);
+
+typedef struct fs_mx4_plan_s *fs_mx4_plan_t; /* opaque; host memory owned by the library */
+
+typedef struct {
+    int64_t shard_blocks;    /* blocks of a rank's quantised shard */
+    int64_t shard_bytes;     /* its bytes: 17 * shard_blocks, rounded up to 128 */
+    int64_t gathered_bytes;  /* N * shard_bytes: the all-gather output */
+    int64_t workspace_bytes; /* device bytes fs_mx4_plan_upload needs */
+} fs_mx4_plan_info_t;
+
+/*
+ * fs_mx4_plan -- lay out a group's quantised shards (host only).
+ *
+ * Every run of fs_plan_segments (one parameter's elements on one rank) is cut
+ * into blocks from its own first element and starts on a multiple of 8
+ * blocks of its rank's shard, so no block mixes parameters and the codes
+ * start on 128 bytes.  FSDP2: parameter i starts at the same block on every rank
+ * (its chunk counted whole); FSDP1: the rank's runs follow each other, and
+ * every shard has the longest one's blocks.  A rank's shard is its blocks'
+ * codes, then their scales; blocks of no run and the bytes up to shard_bytes
+ * are zero after fs_pack_mx4.  The plan may be destroyed afterwards.
+ * Errors: FS_E_INVAL (NULL), FS_E_OVERFLOW, FS_E_NOMEM.
+ */
+int fs_mx4_plan(fs_plan_t plan, fs_mx4_plan_t *out);
+int fs_mx4_plan_info(fs_mx4_plan_t p, fs_mx4_plan_info_t *out);
+/* First block of parameter i's run in rank r's shard, and its element count (0: none). */
+int fs_mx4_plan_piece(fs_mx4_plan_t p, int32_t i, int32_t rank, int64_t *first_block, int64_t *numel);
+/* As fs_plan_upload. */
+int fs_mx4_plan_upload(fs_mx4_plan_t p, void *workspace, size_t bytes, hipStream_t stream);
+void fs_mx4_plan_destroy(fs_mx4_plan_t p);
+
+/*
+ * fs_mx4_plan_matrix -- parameter i of a gathered buffer as a matrix of d0
+ * rows (host only; nothing is read), for fs_mx4_matmul and fs_mx4_dequantize.
+ * Needs an FSDP2 plan, whose chunks are whole rows, and rows of whole blocks.
+ * Errors: FS_E_INVAL (NULL, i out of range), FS_E_ALIGN (gathered not 16-byte
+ * aligned), FS_E_UNSUPPORTED (FSDP1, or rows that are not a multiple of 32).
+ */
+int fs_mx4_plan_matrix(fs_mx4_plan_t p, void *gathered, int32_t i, fs_mx4_matrix_t *out);
+
+/*
+ * fs_pack_mx4 -- the all-gather copy-in in 4 bits, as fs_pack and
+ * fs_pack_cast.
+ *
+ *   params (device) array of n_params device pointers to numel_i contiguous
+ *                   elements of param_dtype.
+ *   out    (device) 16-byte aligned; rank < 0: gathered_bytes, rank r: r's
+ *                   shard_bytes.  Every byte is written.
+ *   seed   (device) as in fs_mx4_quantize, orientation 0; a block's index is
+ *                   rank * shard_blocks + its place in the shard, so one rank's
+ *                   pack gives the bytes that the whole one gives.
+ * Errors: FS_E_INVAL (not uploaded, rank out of range, NULL), FS_E_DTYPE,
+ * FS_E_ALIGN, FS_E_OVERFLOW, FS_E_HIP.
+ */
+int fs_pack_mx4(fs_mx4_plan_t p, const void *const *params, fs_dtype param_dtype, void *out,
+                int32_t rank, const uint64_t *seed, hipStream_t stream);
+
+/*
+ * fs_unpack_mx4 -- the all-gather copy-out: gathered -> params (device array
+ * of n_params device pointers), numel_i elements of param_dtype each, rounded
+ * as in fs_mx4_dequantize.  Errors: as fs_pack_mx4.
+ */
+int fs_unpack_mx4(fs_mx4_plan_t p, const void *gathered, void *const *params, fs_dtype param_dtype,
+                  hipStream_t stream);
+
+/*
+ * fs_reduce_shard_mx4 -- fs_reduce_shard over quantised slices.
+ *
+ *   rank            whose shard it is.
+ *   grad_acc        A >= 1.
+ *   slices (host)   array of A*N device pointers, 16-byte aligned; slices[j*N + k]
+ *                   is logical rank k's quantised gradient at micro-step j,
+ *                   restricted to this rank's shard (shard_bytes, as
+ *                   fs_pack_mx4 with this rank writes them).
+ *   out   (device)  the plan's shard_numel fp32 values, at the plan's element
+ *                   positions (what fs_adamw_step takes): the A*N values of
+ *                   an element are added in fp32 one by one in slice order and
+ *                   the sum divided once by N; pads are zero.  Bit-exact and
+ *                   deterministic.
+ * Errors: as fs_reduce_shard; FS_E_INVAL (not uploaded, rank out of range).
+ */
+int fs_reduce_shard_mx4(fs_mx4_plan_t p, int32_t rank, int32_t grad_acc,
+                        const void *const *slices, float *out, hipStream_t stream);
+
 /* fs_last_error -- message for the calling thread's last failed call
  * (empty string if none).  The pointer stays valid until the next call. */
 const char *fs_last_error(void);

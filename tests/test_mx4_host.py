@@ -1,0 +1,266 @@
+"""Microscaled 4-bit shards without a GPU: the layout of the quantised shards
+against its definition, parameters as matrices, workspace sizes, and the
+refusals of every call (each is refused before anything is launched)."""
+import ctypes
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import fsdp_sharded_state_amd as fs
+import mx4_ref as ref
+import synth
+
+LISTS = {
+    "mlp": synth.mlp_tiny_shapes(),
+    "odd": [(5, 7), (1,), (), (0, 4), (33,), (3, 32), (100, 64), (2, 5, 9), (257,)],
+    "empty": [],
+    "none": [(0,), (0, 3)],
+    "tiny": [(1,)] * 20,
+    "long": [(3, 8192), (40000,)],
+}
+
+
+def _plans():
+    for name, shapes in LISTS.items():
+        for world in (1, 2, 3, 8):
+            for mode, orig in (("fsdp1", False), ("fsdp1", True), ("fsdp2", False)):
+                yield name, shapes, world, mode, orig
+
+
+@pytest.mark.parametrize("name,shapes,world,mode,orig", list(_plans()))
+def test_layout(name, shapes, world, mode, orig):
+    plan = fs.fs_plan(shapes, "bf16", world, orig, mode)
+    mp = fs.fs_mx4_plan(plan)
+    rows = [(plan.param(i).chunk_rows, plan.param(i).row) for i in range(len(shapes))]
+    pieces, blocks, nbytes = ref.layout(plan.segments(), rows, mode, world, len(shapes))
+    assert (mp.shard_blocks, mp.shard_bytes, mp.gathered_bytes) == (blocks, nbytes, world * nbytes)
+    for i in range(len(shapes)):
+        for r in range(world):
+            b, n = mp.piece(i, r)
+            want = pieces.get((i, r))
+            assert n == (want[2] if want else 0)
+            if want:
+                assert b == want[0] and b % 8 == 0
+    # pieces do not overlap and lie in the shard
+    for r in range(world):
+        used = sorted((b, b + ref.blocks(n)) for (p, rr), (b, _, n) in pieces.items() if rr == r)
+        assert all(x[1] <= y[0] for x, y in zip(used, used[1:])) and (not used or used[-1][1] <= blocks)
+
+
+def test_layout_of_both_element_types_and_the_twin():
+    """FSDP1 with use_orig_params aligns by the element size: the quantised layout follows the plan's segments."""
+    for dtype in ("bf16", "fp32"):
+        plan = fs.fs_plan([(5,), (7, 3), (64,)], dtype, 3, True, "fsdp1")
+        mp, twin = fs.fs_mx4_plan(plan), fs.fs_mx4_plan(plan.twin("fp32"))
+        pieces, blocks, nbytes = ref.layout(plan.segments(), None, "fsdp1", 3, 3)
+        for m in (mp, twin):
+            assert (m.shard_blocks, m.shard_bytes) == (blocks, nbytes)
+            assert {k: m.piece(*k) for k in pieces} == {k: (v[0], v[2]) for k, v in pieces.items()}
+
+
+def test_random_layouts():
+    rng = random.Random(11)
+    for _ in range(150):
+        shapes = [tuple(rng.randint(0, 40) for _ in range(rng.randint(0, 3))) for _ in range(rng.randint(0, 6))]
+        world, (mode, orig) = rng.randint(1, 9), rng.choice([("fsdp1", False), ("fsdp1", True), ("fsdp2", False)])
+        plan = fs.fs_plan(shapes, rng.choice(["bf16", "fp32"]), world, orig, mode)
+        mp = fs.fs_mx4_plan(plan)
+        rows = [(plan.param(i).chunk_rows, plan.param(i).row) for i in range(len(shapes))]
+        pieces, blocks, nbytes = ref.layout(plan.segments(), rows, mode, world, len(shapes))
+        assert (mp.shard_blocks, mp.shard_bytes) == (blocks, nbytes)
+        for k, v in pieces.items():
+            assert mp.piece(*k) == (v[0], v[2])
+
+
+def test_plan_outlives_the_group_plan():
+    plan = fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2")
+    h = ctypes.c_void_p()
+    assert fs.lib().fs_mx4_plan(plan._h, ctypes.byref(h)) == 0
+    plan.close()
+    b, n = ctypes.c_int64(), ctypes.c_int64()
+    assert fs.lib().fs_mx4_plan_piece(h, 0, 1, ctypes.byref(b), ctypes.byref(n)) == 0 and n.value == 4 * 64
+    fs.lib().fs_mx4_plan_destroy(h)
+    fs.lib().fs_mx4_plan_destroy(None)
+
+
+def test_plan_refusals():
+    L, h = fs.lib(), ctypes.c_void_p()
+    plan = fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2")
+    mp = fs.fs_mx4_plan(plan)
+    n = ctypes.c_int64()
+    assert L.fs_mx4_plan(None, ctypes.byref(h)) == fs.FS_E_INVAL
+    assert L.fs_mx4_plan(plan._h, None) == fs.FS_E_INVAL
+    assert L.fs_mx4_plan_info(None, None) == fs.FS_E_INVAL
+    for i, r in ((-1, 0), (1, 0), (0, -1), (0, 2)):
+        assert L.fs_mx4_plan_piece(mp._h, i, r, ctypes.byref(n), ctypes.byref(n)) == fs.FS_E_INVAL
+    assert L.fs_mx4_plan_upload(mp._h, None, 1 << 20, None) == fs.FS_E_INVAL
+    assert L.fs_mx4_plan_upload(mp._h, 1 << 20 | 8, 1 << 20, None) == fs.FS_E_ALIGN
+    assert L.fs_mx4_plan_upload(mp._h, 1 << 20, 8, None) == fs.FS_E_INVAL
+
+
+def test_matrix_of_a_parameter():
+    shapes = [(64,), (11, 96), (5, 33), (4, 2, 64), (0, 32), (3, 0)]
+    mp = fs.fs_mx4_plan(fs.fs_plan(shapes, "bf16", 4, False, "fsdp2"))
+    L, m, base = fs.lib(), fs.Mx4MatrixStruct(), 1 << 20
+    assert L.fs_mx4_plan_matrix(mp._h, base, 1, ctypes.byref(m)) == 0
+    b = mp.piece(1, 0)[0]
+    assert (m.codes, m.scales) == (base + 16 * b, base + 16 * mp.shard_blocks + b)
+    assert (m.rows, m.cols, m.code_stride, m.scale_stride, m.chunk_rows, m.chunk_stride) == (11, 96, 48, 3, 3, mp.shard_bytes)
+    assert L.fs_mx4_plan_matrix(mp._h, base, 3, ctypes.byref(m)) == 0 and (m.rows, m.cols) == (4, 128)
+    assert L.fs_mx4_plan_matrix(mp._h, base, 4, ctypes.byref(m)) == 0 and m.rows == 0
+    assert L.fs_mx4_plan_matrix(mp._h, base, 5, ctypes.byref(m)) == 0 and (m.rows, m.cols) == (0, 0)
+    for i, code in ((0, fs.FS_E_UNSUPPORTED), (2, fs.FS_E_UNSUPPORTED), (-1, fs.FS_E_INVAL), (6, fs.FS_E_INVAL)):
+        assert L.fs_mx4_plan_matrix(mp._h, base, i, ctypes.byref(m)) == code
+    assert L.fs_mx4_plan_matrix(mp._h, base + 8, 1, ctypes.byref(m)) == fs.FS_E_ALIGN
+    assert L.fs_mx4_plan_matrix(mp._h, None, 1, ctypes.byref(m)) == fs.FS_E_INVAL
+    one = fs.fs_mx4_plan(fs.fs_plan(shapes, "bf16", 4, False, "fsdp1"))
+    assert L.fs_mx4_plan_matrix(one._h, base, 1, ctypes.byref(m)) == fs.FS_E_UNSUPPORTED
+
+
+def test_calls_on_a_plan_without_tables_are_refused():
+    mp = fs.fs_mx4_plan(fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2"))
+    L = fs.lib()
+    p = (ctypes.c_void_p * 2)(1 << 20, 1 << 21)
+    assert L.fs_pack_mx4(mp._h, 1 << 20, 0, 1 << 21, -1, None, None) == fs.FS_E_INVAL
+    assert b"fs_mx4_plan_upload" in L.fs_last_error()
+    assert L.fs_unpack_mx4(mp._h, 1 << 20, 1 << 21, 0, None) == fs.FS_E_INVAL
+    assert L.fs_reduce_shard_mx4(mp._h, 0, 1, p, 1 << 22, None) == fs.FS_E_INVAL
+    for call in (lambda: L.fs_pack_mx4(None, 1, 0, 1, -1, None, None), lambda: L.fs_unpack_mx4(None, 1, 1, 0, None),
+                 lambda: L.fs_reduce_shard_mx4(None, 0, 1, p, 1, None)):
+        assert call() == fs.FS_E_INVAL
+
+
+X, C, S, T, U, SEED, WS = (1 << 20, 1 << 30, (1 << 30) + (1 << 29), 1 << 31, (1 << 31) + (1 << 29), 1 << 12, 1 << 33)
+
+
+def _mat(codes=C, scales=S, rows=40, cols=70, cs=48, ss=3, chunk=0, stride=0):
+    return ctypes.byref(fs.Mx4MatrixStruct(codes, scales, rows, cols, cs, ss, chunk, stride))
+
+
+def _quantize(rows=40, cols=70, x=X, dtype=0, ldx=70, by_row="ok", by_col=None, seed=None):
+    by_row = _mat() if by_row == "ok" else by_row
+    return fs.lib().fs_mx4_quantize(rows, cols, x, dtype, ldx, by_row, by_col, seed, None)
+
+
+COL = dict(codes=T, scales=U, rows=70, cols=40, cs=32, ss=2)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), fs.FS_E_INVAL), (dict(cols=-1), fs.FS_E_INVAL), (dict(x=None), fs.FS_E_INVAL),
+    (dict(dtype=2), fs.FS_E_DTYPE), (dict(x=X + 1), fs.FS_E_ALIGN), (dict(x=X + 2, dtype=1), fs.FS_E_ALIGN),
+    (dict(ldx=69), fs.FS_E_INVAL), (dict(ldx=1 << 60), fs.FS_E_OVERFLOW), (dict(by_row=None), fs.FS_E_INVAL),
+    (dict(rows=1 << 31, by_row=_mat(rows=1 << 31)), fs.FS_E_OVERFLOW),
+    (dict(seed=SEED + 4), fs.FS_E_ALIGN),
+    (dict(by_row=_mat(rows=41)), fs.FS_E_INVAL), (dict(by_row=_mat(cols=71)), fs.FS_E_INVAL),
+    (dict(by_row=_mat(codes=None)), fs.FS_E_INVAL), (dict(by_row=_mat(scales=None)), fs.FS_E_INVAL),
+    (dict(by_row=_mat(codes=C + 8)), fs.FS_E_ALIGN), (dict(by_row=_mat(cs=56)), fs.FS_E_ALIGN),
+    (dict(by_row=_mat(cs=32)), fs.FS_E_INVAL), (dict(by_row=_mat(ss=2)), fs.FS_E_INVAL),
+    (dict(by_row=_mat(chunk=10, stride=4096)), fs.FS_E_INVAL),
+    (dict(by_row=_mat(codes=X - 16)), fs.FS_E_INVAL), (dict(by_row=_mat(scales=X + 5)), fs.FS_E_INVAL),
+    (dict(by_row=_mat(scales=C + 100)), fs.FS_E_INVAL),                     # inside its own codes
+    (dict(by_row=_mat(codes=SEED & ~15), seed=SEED), fs.FS_E_INVAL),
+    (dict(by_col=_mat(**{**COL, "rows": 69})), fs.FS_E_INVAL), (dict(by_col=_mat(**{**COL, "codes": C + 160})), fs.FS_E_INVAL),
+    (dict(by_col=_mat(**{**COL, "scales": S})), fs.FS_E_INVAL), (dict(by_row=_mat(cs=1 << 60)), fs.FS_E_OVERFLOW),
+    (dict(rows=2 ** 31 - 1, cols=2 ** 31 - 1, ldx=2 ** 31 - 1, x=1 << 12,      # more tiles than a grid holds
+          by_row=_mat(rows=2 ** 31 - 1, cols=2 ** 31 - 1, codes=1 << 63, scales=3 << 62, cs=1 << 30, ss=1 << 26)), fs.FS_E_OVERFLOW),
+])
+def test_quantize_refusals(kw, code):
+    assert _quantize(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_mx4_quantize")
+
+
+def test_quantize_of_nothing_needs_no_memory():
+    for rows, cols in ((0, 5), (5, 0), (0, 0)):
+        assert _quantize(rows=rows, cols=cols, x=None, ldx=0, by_row=_mat(None, None, rows, cols, 0, 0)) == 0
+
+
+def _dequantize(m="ok", out=X, dtype=1, ldo=70):
+    return fs.lib().fs_mx4_dequantize(_mat() if m == "ok" else m, out, dtype, ldo, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(m=None), fs.FS_E_INVAL), (dict(out=None), fs.FS_E_INVAL), (dict(dtype=5), fs.FS_E_DTYPE), (dict(out=X + 2), fs.FS_E_ALIGN),
+    (dict(ldo=69), fs.FS_E_INVAL), (dict(out=C), fs.FS_E_INVAL), (dict(out=S - 4), fs.FS_E_INVAL),
+    (dict(m=_mat(chunk=-1)), fs.FS_E_INVAL), (dict(m=_mat(chunk=10, stride=1000)), fs.FS_E_ALIGN),
+    (dict(m=_mat(chunk=10, stride=464)), fs.FS_E_INVAL),                    # chunks overlap
+    (dict(m=_mat(chunk=10, stride=1 << 60)), fs.FS_E_OVERFLOW),
+    (dict(m=_mat(chunk=10, stride=4096), out=C + 4096 * 3), fs.FS_E_INVAL),  # in the last chunk
+    (dict(m=_mat(rows=-1)), fs.FS_E_INVAL), (dict(m=_mat(cols=1 << 40)), fs.FS_E_OVERFLOW),
+])
+def test_dequantize_refusals(kw, code):
+    assert _dequantize(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_mx4_dequantize")
+
+
+def _matmul(a="ok", b="ok", out=X, dtype=1, ldo=50, ws=WS, nbytes=1 << 40):
+    a = _mat() if a == "ok" else a
+    b = _mat(codes=T, scales=U, rows=50) if b == "ok" else b
+    return fs.lib().fs_mx4_matmul(a, b, out, dtype, ldo, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(a=None), fs.FS_E_INVAL), (dict(b=None), fs.FS_E_INVAL), (dict(out=None), fs.FS_E_INVAL), (dict(dtype=2), fs.FS_E_DTYPE),
+    (dict(out=X + 2), fs.FS_E_ALIGN), (dict(out=X + 1, dtype=0), fs.FS_E_ALIGN), (dict(ldo=49), fs.FS_E_INVAL),
+    (dict(a=_mat(cols=71)), fs.FS_E_INVAL), (dict(out=C + 64), fs.FS_E_INVAL), (dict(out=S), fs.FS_E_INVAL),
+    (dict(out=T + 64), fs.FS_E_INVAL), (dict(out=U), fs.FS_E_INVAL), (dict(a=_mat(codes=C + 4)), fs.FS_E_ALIGN),
+    (dict(b=_mat(codes=None, rows=50)), fs.FS_E_INVAL), (dict(a=_mat(rows=-1)), fs.FS_E_INVAL), (dict(ldo=1 << 60), fs.FS_E_OVERFLOW),
+])
+def test_matmul_refusals(kw, code):
+    assert _matmul(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_mx4_matmul")
+
+
+def test_matmul_workspace_refusals():
+    L, n = fs.lib(), ctypes.c_int64()
+    assert L.fs_mx4_matmul_workspace(1, 1, 1, None) == fs.FS_E_INVAL
+    for m, k in ((-1, 1), (1, -1)):
+        assert L.fs_mx4_matmul_workspace(m, 5, k, ctypes.byref(n)) == fs.FS_E_INVAL
+    assert L.fs_mx4_matmul_workspace(1 << 31, 5, 5, ctypes.byref(n)) == fs.FS_E_OVERFLOW
+    for m, nn, k in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (1, 1, 1), (8192, 8192, 8192), (64, 64, 1 << 20)):
+        assert L.fs_mx4_matmul_workspace(m, nn, k, ctypes.byref(n)) == 0 and n.value >= 0
+
+
+def test_binding_refusals():
+    """What the binding checks itself; nothing reaches the library."""
+    host = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU"):
+        fs.Mx4Matrix(host, torch.zeros(4, 2, dtype=torch.uint8), 64)
+    with pytest.raises(ValueError, match="codes"):
+        fs.Mx4Matrix(host, torch.zeros(4, 2, dtype=torch.uint8), 65)
+    with pytest.raises(ValueError, match="GPU"):
+        fs.fs_mx4_quantize(torch.zeros(3, 3))
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        fs.fs_mx4_quantize(torch.zeros(3, 3, dtype=torch.float16))
+    mp = fs.fs_mx4_plan(fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2"))
+    with pytest.raises(ValueError, match="uint8"):
+        fs.fs_pack_mx4(mp, [torch.zeros(8, 64)], torch.zeros(5, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="GPU"):
+        fs.fs_pack_mx4(mp, [torch.zeros(8, 64)], torch.zeros(mp.gathered_bytes, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="slices"):
+        fs.fs_reduce_shard_mx4(mp, [], torch.zeros(4 * 64), rank=0)
+    with pytest.raises(ValueError, match="float32"):
+        fs.fs_reduce_shard_mx4(mp, [], torch.zeros(5), rank=0)
+
+
+# ------------------------------------------------- the definition's own pins --
+
+def test_reference_against_hand_worked_blocks():
+    x = np.zeros((5, 32))
+    x[0, :10] = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, 4.0, 7.9]     # amax 7.9: scale 1; ties to even; 7.9 saturates
+    x[1, :3] = [1.0, -0.0, 0.1]                                             # amax 1: scale 1/4
+    x[2, 0] = 2.0 ** -149                                                   # below every scale
+    x[3, 5] = np.inf
+    x[4, 0], x[4, 1] = 3.4028234663852886e38, 2.0 ** 125 * 5
+    c, s = ref.encode(x)
+    assert list(s) == [127, 125, 0, 255, 252]
+    v = ref.decode(c, s[:, None])
+    assert list(v[0, :10]) == [0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, -0.0, 4.0, 6.0]
+    assert np.signbit(v[0, 7]) and np.signbit(v[1, 1]) and v[1, 0] == 1.0 and v[1, 2] == 0.125
+    assert np.all(v[2] == 0) and np.all(np.isnan(v[3])) and v[4, 0] == 6 * 2.0 ** 125 and v[4, 1] == 4 * 2.0 ** 125
+    c, s = ref.encode(x[[0, 1, 3]], seed=5, block_index=[0, 1, 2])          # stochastic: 7.9 > 6 takes the next scale
+    assert list(s) == [128, 125, 255]
+
+
+def test_philox_known_answers():
+    """The generator's published 7-round answer for key and counter of zeros."""
+    z = ref.philox(0, [0], 0)[0]
+    assert [hex(int(v)) for v in z] == ["0x5f6fb709", "0xd893f64", "0x4f121f81", "0x4f730a48"]
