@@ -232,16 +232,20 @@ __device__ __forceinline__ void store8(float *p, uint32_t c, float scale, int va
     store8(p, v, valid);
 }
 
-// A matrix of blocks, by value.
+// A matrix of blocks, by value.  Rows fit in 31 bits, so a row's chunk comes
+// from a multiplication: with l = ceil(log2(chunk_rows)) and
+// mul = floor(2^(31+l) / chunk_rows) + 1, which is under 2^32,
+// r / chunk_rows = r * mul >> (31 + l) for every r under 2^31.
 struct Mx4Mat {
     const uint8_t *codes, *scales;
-    int64_t code_stride, scale_stride, chunk_rows, chunk_stride;
+    int64_t code_stride, scale_stride, chunk_stride;
+    uint32_t chunk_rows, chunk_mul, chunk_shift;   // chunk_rows 0: the rows are one run
 
     // Byte offsets of a row's codes and scales.
-    __device__ __forceinline__ void row(int64_t r, int64_t *code, int64_t *scale) const {
+    __device__ __forceinline__ void row(uint32_t r, int64_t *code, int64_t *scale) const {
         int64_t base = 0;
         if (chunk_rows) {
-            const int64_t c = r / chunk_rows;
+            const uint32_t c = (uint32_t)((uint64_t)r * chunk_mul >> chunk_shift);
             base = c * chunk_stride;
             r -= c * chunk_rows;
         }

@@ -202,7 +202,7 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
         const int64_t r = r0 + q / kMatQuarters, c = c0 + 8 * (q % kMatQuarters);
         if (r >= rows || c >= cols) continue;
         int64_t code, scale;
-        m.row(r, &code, &scale);
+        m.row((uint32_t)r, &code, &scale);
         const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
         store8(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
     }
@@ -409,8 +409,14 @@ int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, M
     out->scales = static_cast<const uint8_t *>(m->scales);
     out->code_stride = run > 1 ? m->code_stride : 0;
     out->scale_stride = run > 1 ? m->scale_stride : 0;
-    out->chunk_rows = chunks > 1 ? m->chunk_rows : 0;
-    out->chunk_stride = chunks > 1 ? m->chunk_stride : 0;
+    if (chunks > 1) {
+        uint32_t l = 0;
+        while (((int64_t)1 << l) < m->chunk_rows) ++l;   // chunk_rows < rows < 2^31
+        out->chunk_rows = (uint32_t)m->chunk_rows;
+        out->chunk_shift = 31 + l;
+        out->chunk_mul = (uint32_t)(((uint64_t)1 << (31 + l)) / (uint64_t)m->chunk_rows + 1);
+        out->chunk_stride = m->chunk_stride;
+    }
     return FS_OK;
 }
 
