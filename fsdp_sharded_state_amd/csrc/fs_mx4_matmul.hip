@@ -13,19 +13,18 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 // The scaled matrix instruction on 16 by 16 outputs and 128 elements of k:
-// lane l holds row l%16 and block l/16 of the four, its scale in byte BX
-// (BY) of the scale register; output element i of lane l is (row 4*(l/16) + i of the
+// lane l holds row l%16 and block l/16 of the four, its scale in byte 0 of
+// the scale register; output element i of lane l is (row 4*(l/16) + i of the
 // first operand, row l%16 of the second).  The second operand is taken from
 // `a`, so that a lane's four outputs are consecutive in a row of `out`.
-template <int BX, int BY>
-__device__ __forceinline__ f32x4 mfma16x(u32x4 x, uint32_t sx, u32x4 y, uint32_t sy, f32x4 acc) {
+__device__ __forceinline__ f32x4 mfma16(u32x4 x, uint32_t sx, u32x4 y, uint32_t sy, f32x4 acc) {
     const i32x8 p = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
     const i32x8 q = {(int)y.x, (int)y.y, (int)y.z, (int)y.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, acc, 4, 4, BX, (int)sx, BY, (int)sy);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(p, q, acc, 4, 4, 0, (int)sx, 0, (int)sy);
 }
 
 // The same on 32 by 32 outputs and 64 elements of k: lane l holds row l%32 and
-// block l/32; its output 4*g + e is row 8*g + 4*(l/32) + e of the first operand, row l%32 of the second.
+// block l/32 of two, its scale in byte BX (BY); its output 4*g + e is row 8*g + 4*(l/32) + e of the first operand, row l%32 of the second.
 template <int BX, int BY>
 __device__ __forceinline__ f32x16 mfma32(u32x4 x, uint32_t sx, u32x4 y, uint32_t sy, f32x16 acc) {
     const i32x8 p = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
@@ -53,47 +52,120 @@ __device__ __forceinline__ void store4(uint16_t *p, f32x4 v, int64_t valid) {
     }
 }
 
-// Each wave takes 32 by 32 outputs, a workgroup 64 by 64, fragments straight
-// from memory.  Rows beyond the matrices read the last one, and are not stored.
-template <class T>
-__global__ __launch_bounds__(256) void matmul_mx4_kernel(Mx4Mat a, Mx4Mat b, int64_t m, int64_t n, int64_t nb,
-                                                         T *__restrict__ out, int64_t ldo, uint32_t tiles_n) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, kb = lane >> 4;
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * 64 + (wave >> 1) * 32;
-    const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 64 + (wave & 1) * 32;
-    int64_t ac[2], as[2], bc[2], bs[2];
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own, and the grid is a
+// multiple of 8 or there is a workgroup for every tile: tile `id` is on XCD id % 8.  An XCD
+// takes a run of the tile order, in which kGroup tiles down are taken before the
+// next column, so the tiles that it works on at a time share rows of both.
+constexpr uint32_t kXcds = 8, kGroup = 4;
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t *tm, uint32_t *tn) {
+    const uint32_t total = tiles_m * tiles_n, each = total / kXcds, rest = total % kXcds;
+    const uint32_t xcd = id % kXcds, k = id / kXcds;
+    const uint32_t at = xcd * each + (xcd < rest ? xcd : rest) + k;   // the first `rest` XCDs have one more
+    const uint32_t band = at / (kGroup * tiles_n), in = at % (kGroup * tiles_n);
+    const uint32_t high = tiles_m - band * kGroup < kGroup ? tiles_m - band * kGroup : kGroup;
+    *tm = band * kGroup + in % high;
+    *tn = in / high;
+}
+
+// ------------------------------------------------------------ small products --
+//
+// A workgroup takes 16*FM by 16*FN outputs, and its KW waves share k: wave w
+// takes the groups w, w + KW, ... of 16 blocks (four matrix instructions
+// deep), fragments straight from memory, all of a group's loads on their way
+// at once.  So small products fill the chip, and a single token's reads every
+// weight once and no more.  The scales of a row's group come in one load, from
+// which each quarter of the wave takes its byte.  The waves' sums are joined
+// through LDS, in an order that the sizes alone give.  Rows beyond the matrices read the
+// last one, and are not stored.
+template <int FM_, int FN_, int KW_>
+struct SmallShape {
+    static constexpr int FM = FM_, FN = FN_, KW = KW_, kThreads = 64 * KW;
+};
+
+template <class T, class S>
+__global__ __launch_bounds__(S::kThreads) void matmul_mx4_small_kernel(Mx4Mat a, Mx4Mat b, int64_t m, int64_t n, int32_t nb,
+                                                                       T *__restrict__ out, int64_t ldo, uint32_t tiles_m,
+                                                                       uint32_t tiles_n) {
+    constexpr int FM = S::FM, FN = S::FN, F = FM + FN, KW = S::KW, kEntries = FM * FN * 64;
+    __shared__ f32x4 sums[KW / 2][kEntries];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
+    uint32_t tm, tn;
+    tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+    const int64_t m0 = (int64_t)tm * 16 * FM, n0 = (int64_t)tn * 16 * FN;
+    const uint8_t *code[F], *scale[F];   // of a's rows, then b's
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        a.row((uint32_t)imin(m0 + 16 * i + r, m - 1), &ac[i], &as[i]);
-        b.row((uint32_t)imin(n0 + 16 * i + r, n - 1), &bc[i], &bs[i]);
+    for (int i = 0; i < F; ++i) {
+        int64_t c, q;
+        if (i < FM) a.row((uint32_t)imin(m0 + 16 * i + r, m - 1), &c, &q);
+        else b.row((uint32_t)imin(n0 + 16 * (i - FM) + r, n - 1), &c, &q);
+        code[i] = (i < FM ? a.codes : b.codes) + c + kb * kMx4BlockBytes;
+        scale[i] = (i < FM ? a.scales : b.scales) + q;
     }
-    f32x4 acc[2][2] = {};
-    for (int64_t k = kb; k - kb < nb; k += 4) {
-        u32x4 x[2], y[2];
-        uint32_t sx[2], sy[2];
+    f32x4 acc[FN][FM] = {};
+    auto multiply = [&](const u32x4 (&v)[4][F], const uint32_t (&s)[4][F]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x[i] = y[i] = u32x4{0, 0, 0, 0};
-            sx[i] = sy[i] = 127;
-            if (k < nb) {
-                x[i] = *reinterpret_cast<const u32x4 *>(b.codes + bc[i] + k * kMx4BlockBytes);
-                y[i] = *reinterpret_cast<const u32x4 *>(a.codes + ac[i] + k * kMx4BlockBytes);
-                sx[i] = b.scales[bs[i] + k];
-                sy[i] = a.scales[as[i] + k];
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = mfma16(v[t][FM + i], s[t][FM + i], v[t][j], s[t][j], acc[i][j]);
+    };
+    const int32_t whole = nb & ~15;
+    for (int32_t k0 = 16 * wave; k0 < whole; k0 += 16 * KW) {
+        u32x4 v[4][F], q[F];
+        uint32_t s[4][F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            q[i] = ld16_any(scale[i] + k0);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) v[t][i] = *reinterpret_cast<const u32x4 *>(code[i] + (int64_t)(k0 + 4 * t) * kMx4BlockBytes);
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) s[t][i] = word(q[i], t) >> (8 * kb);
+        multiply(v, s);
+    }
+    if (whole < nb && (whole >> 4) % KW == wave) {   // the last group, block by block
+        u32x4 v[4][F];
+        uint32_t s[4][F];
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                v[t][i] = u32x4{0, 0, 0, 0};
+                s[t][i] = 127;
+                if (whole + 4 * t + kb < nb) {
+                    v[t][i] = *reinterpret_cast<const u32x4 *>(code[i] + (int64_t)(whole + 4 * t) * kMx4BlockBytes);
+                    s[t][i] = scale[i][whole + 4 * t + kb];
+                }
             }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) acc[i][j] = mfma16x<0, 0>(x[i], sx[i], y[j], sy[j], acc[i][j]);
+        multiply(v, s);
     }
+    // the upper waves' sums to the lower ones, then theirs to all
+    auto entry = [&](int i, int j) { return (i * FM + j) * 64 + lane; };
+    if (wave >= KW / 2) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int64_t row = m0 + 16 * j + r, col = n0 + 16 * i + 4 * kb;
-            if (row < m && col < n) store4(out + row * ldo + col, acc[i][j], n - col);
-        }
+            for (int j = 0; j < FM; ++j) sums[wave - KW / 2][entry(i, j)] = acc[i][j];
+    }
+    __syncthreads();
+    if (wave < KW / 2) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) sums[wave][entry(i, j)] += acc[i][j];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < kEntries; e += S::kThreads) {
+        f32x4 v = sums[0][e];
+#pragma unroll
+        for (int w = 1; w < KW / 2; ++w) v += sums[w][e];
+        const int frag = e >> 6, l = e & 63;
+        const int64_t row = m0 + 16 * (frag % FM) + (l & 15), col = n0 + 16 * (frag / FM) + 4 * (l >> 4);
+        if (row < m && col < n) store4(out + row * ldo + col, v, n - col);
+    }
 }
 
 // ------------------------------------------------------------ large products --
@@ -123,25 +195,9 @@ __global__ __launch_bounds__(256) void matmul_mx4_kernel(Mx4Mat a, Mx4Mat b, int
 // the start of a tile nor the writing of its outputs leaves the loads idle.
 // Outputs go through LDS, a part of a wave's tile at a time, so that stores cover whole cache lines.
 
-// Workgroups go to the 8 XCDs in turn, each with an L2 of its own, and the grid is a
-// multiple of 8 or there is a workgroup for every tile: tile `id` is on XCD id % 8.  An XCD
-// takes a run of the tile order, in which kGroup tiles down are taken before the
-// next column, so the tiles that it works on at a time share rows of both.
-constexpr uint32_t kXcds = 8, kGroup = 4;
-__device__ __forceinline__ void big_tile(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t *tm, uint32_t *tn) {
-    const uint32_t total = tiles_m * tiles_n, each = total / kXcds, rest = total % kXcds;
-    const uint32_t xcd = id % kXcds, k = id / kXcds;
-    const uint32_t at = xcd * each + (xcd < rest ? xcd : rest) + k;   // the first `rest` XCDs have one more
-    const uint32_t band = at / (kGroup * tiles_n), in = at % (kGroup * tiles_n);
-    const uint32_t high = tiles_m - band * kGroup < kGroup ? tiles_m - band * kGroup : kGroup;
-    *tm = band * kGroup + in % high;
-    *tn = in / high;
-}
-
 constexpr int kStepBlocks = 4;       // blocks of k in a step
 constexpr int kStepBytes = kStepBlocks * kMx4BlockBytes;
 constexpr int kStages = 4;           // steps in LDS
-constexpr int kBigMinBlocks = kStages * kStepBlocks;   // shorter rows go to the other kernel
 // A tile's rows are addressed by 32-bit offsets from its first one.
 constexpr int64_t kBigMaxOffset = (int64_t)1 << 31;
 
@@ -190,12 +246,13 @@ struct BigShape {
     static constexpr int LM = BM / kWaves / kLoadRows, LN = BN / kWaves / kLoadRows;  // a wave's loads of a step
     static constexpr int kRows = BM + BN, kScaleLoads = (kRows + kThreads - 1) / kThreads;
     static constexpr int kBuf = kRows * kStepBytes, kScales = kRows * 16;
+    static constexpr int kPerCu = 163840 / (kStages * kBuf + 2 * kScales + kWaves * kPartBytes);   // workgroups of a CU, by their LDS
     static_assert(LM * kWaves * kLoadRows == BM && LN * kWaves * kLoadRows == BN && FM * GM * 32 == BM && FN * GN * 32 == BN, "whole fragments and loads");
     static_assert(FN % 2 == 0, "fragments of b come in pairs");
 };
 
 template <class T, class S>
-__global__ __launch_bounds__(S::kThreads, S::kWaves / 4) void matmul_mx4_big_kernel(Mx4Mat a, Mx4Mat b, int64_t m, int64_t n,
+__global__ __launch_bounds__(S::kThreads, S::kWaves * S::kPerCu / 4) void matmul_mx4_big_kernel(Mx4Mat a, Mx4Mat b, int64_t m, int64_t n,
                                                                                     int32_t nb, T *__restrict__ out,
                                                                                     int64_t ldo, uint32_t tiles_m,
                                                                                     uint32_t tiles_n) {
@@ -249,12 +306,23 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves / 4) void matmul_mx4_big_ker
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (LdsPtr)(buf + BM * kStepBytes + (wave * S::LN + k - S::LM) * 1024), 16,
                                                      ob[k - S::LM] | beyond, at, 0, 0);
     };
-    // 16 scales of a row; a last group is loaded so that it ends with the row, and shifted down
+    // 16 scales of a row; a last group is loaded so that it ends with the row, and shifted down.  A row of fewer comes
+    // byte by byte, and needs the same shift.
     u32x4 sv[S::kScaleLoads];
     auto load_scales = [&](int32_t k0) {
         const int32_t first = k0 + 16 <= nb ? k0 : nb - 16;
 #pragma unroll
-        for (int j = 0; j < S::kScaleLoads; ++j) sv[j] = ld16_any(sp[j] + first);
+        for (int j = 0; j < S::kScaleLoads; ++j) {
+            if (nb >= 16) {
+                sv[j] = ld16_any(sp[j] + first);
+            } else {
+                uint32_t w[4] = {};
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (first + k >= 0) w[k >> 2] |= (uint32_t)sp[j][first + k] << (8 * (k & 3));
+                sv[j] = u32x4{w[0], w[1], w[2], w[3]};
+            }
+        }
     };
     auto store_scales = [&](uint8_t *s, int32_t k0) {
         const int over = (int)imax(0, imin(16, k0 + 16 - nb));   // bytes that belong to earlier groups
@@ -390,7 +458,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves / 4) void matmul_mx4_big_ker
 
     const int32_t groups = (nb + 15) / 16;   // of four steps
     uint32_t tile = blockIdx.x, tm, tn;
-    big_tile(tile, tiles_m, tiles_n, &tm, &tn);
+    tile_of(tile, tiles_m, tiles_n, &tm, &tn);
     aim((int64_t)tm * BM, (int64_t)tn * BN);
     load_scales(0);
 #pragma unroll
@@ -428,7 +496,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves / 4) void matmul_mx4_big_ker
             int32_t load = g + 1;   // the group to load
             if (load == groups && more) {
                 tile += gridDim.x;
-                big_tile(tile, tiles_m, tiles_n, &tm, &tn);
+                tile_of(tile, tiles_m, tiles_n, &tm, &tn);
                 aim((int64_t)tm * BM, (int64_t)tn * BN);
                 load = 0;
             }
@@ -454,20 +522,33 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves / 4) void matmul_mx4_big_ker
 #endif
 }
 
-using BigTile = BigShape<256, 256, 4, 2>;
-constexpr int kBig = 256;   // the longer side of a tile
+constexpr int kBig = 256;   // the longest side of a tile
 
-// Workgroups that run at a time: one a CU.
+// Workgroups that run at a time.
+template <class S>
 int64_t big_grid() {
     const CuLimits L = cu_limits();
-    return L.cus > 0 ? L.cus : 256;
+    return (L.cus > 0 ? L.cus : 256) * S::kPerCu;
 }
 
 template <class T, class S>
-void launch_big(const Mx4Mat &a, const Mx4Mat &b, int64_t m, int64_t n, int64_t nb, void *out, int64_t ldo, hipStream_t stream) {
-    const uint32_t tm = (uint32_t)((m + S::BM - 1) / S::BM), tn = (uint32_t)((n + S::BN - 1) / S::BN);
-    hipLaunchKernelGGL((matmul_mx4_big_kernel<T, S>), dim3((uint32_t)imin((int64_t)tm * tn, big_grid())), dim3(S::kThreads), 0, stream, a, b, m, n, (int32_t)nb,
-                       static_cast<T *>(out), ldo, tm, tn);
+int launch_big(const char *what, const Mx4Mat &a, const Mx4Mat &b, int64_t m, int64_t n, int64_t nb, void *out, int64_t ldo,
+               hipStream_t stream) {
+    const int64_t tm = (m + S::BM - 1) / S::BM, tn = (n + S::BN - 1) / S::BN;
+    if (tm * tn > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: too many outputs for one launch", what);
+    hipLaunchKernelGGL((matmul_mx4_big_kernel<T, S>), dim3((uint32_t)imin(tm * tn, big_grid<S>())), dim3(S::kThreads), 0,
+                       stream, a, b, m, n, (int32_t)nb, static_cast<T *>(out), ldo, (uint32_t)tm, (uint32_t)tn);
+    return check_launch(what);
+}
+
+template <class T, class S>
+int launch_small(const char *what, const Mx4Mat &a, const Mx4Mat &b, int64_t m, int64_t n, int64_t nb, void *out, int64_t ldo,
+                 hipStream_t stream) {
+    const int64_t tm = (m + 16 * S::FM - 1) / (16 * S::FM), tn = (n + 16 * S::FN - 1) / (16 * S::FN);
+    if (tm * tn > UINT32_MAX / S::kThreads) return fail(FS_E_OVERFLOW, "%s: too many outputs for one launch", what);
+    hipLaunchKernelGGL((matmul_mx4_small_kernel<T, S>), dim3((uint32_t)(tm * tn)), dim3(S::kThreads), 0, stream, a, b, m, n,
+                       (int32_t)nb, static_cast<T *>(out), ldo, (uint32_t)tm, (uint32_t)tn);
+    return check_launch(what);
 }
 
 // Whether the offsets of a tile's rows fit (those of any 256 consecutive ones).
@@ -529,22 +610,23 @@ extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b,
             if (ranges_overlap(workspace, need, s.p, s.bytes))
                 return fail(FS_E_INVAL, "%s: workspace overlaps a matrix", what);
     }
-    const int64_t tn = (n + 63) / 64, tiles = tn * ((m + 63) / 64);
-    if (tiles > UINT32_MAX / 256) return fail(FS_E_OVERFLOW, "%s: too many outputs for one launch", what);
     const int64_t nb = mx4_blocks(k), ld = m > 1 ? ldo : 0;
     (void)hipGetLastError();
-    if (m > 128 && n > 128 && nb >= kBigMinBlocks && big_offsets(ka, nb) && big_offsets(kb, nb)) {
-        if (dtype == FS_BF16)
-            launch_big<uint16_t, BigTile>(ka, kb, m, n, nb, out, ld, stream);
-        else
-            launch_big<float, BigTile>(ka, kb, m, n, nb, out, ld, stream);
-        return check_launch(what);
-    }
-    if (dtype == FS_BF16)
-        hipLaunchKernelGGL(matmul_mx4_kernel<uint16_t>, dim3((uint32_t)tiles), dim3(256), 0, stream, ka, kb, m, n, nb,
-                           static_cast<uint16_t *>(out), ld, (uint32_t)tn);
-    else
-        hipLaunchKernelGGL(matmul_mx4_kernel<float>, dim3((uint32_t)tiles), dim3(256), 0, stream, ka, kb, m, n, nb,
-                           static_cast<float *>(out), ld, (uint32_t)tn);
-    return check_launch(what);
+    // By the tiles that there are for 256 CUs, measured over m from 1 to 4096, n and k from 512 to 11008 (us, in a graph).
+    // 16 by 16 up to 512 tiles, or where 16 rows are all: 4.4 for 5.9 of the next (1 by 4096 by 4096), 7.1 for 8.9 (1 by
+    //   11008 by 4096), 7.4 for 7.8 (128 by 1024 by 4096); past it 12.0 for 7.9 (256 by 1024 by 4096).
+    // 32 by 32 up to 512: 7.9 for 12.0 (64 by 4096 by 4096), 5.4 for 6.9 (128 by 4096 by 1024); past it 17.0 for 12.4 (64 by
+    //   11008 by 4096), 45 for 31 (1024 by 1024 by 11008).
+    // 128 by 128 while 256 by 256 would give no more than 128: 16.5 for 27.7 (1024 by 4096 by 4096), 29.3 for 31.2 (2048 by 4096
+    //   by 4096); past it 38.9 for 33.9 (1024 by 11008 by 4096), 141 for 109 (4096 by 11008 by 4096).
+    auto tiles = [&](int64_t side) { return ((m + side - 1) / side) * ((n + side - 1) / side); };
+    const bool offsets = big_offsets(ka, nb) && big_offsets(kb, nb);
+    auto go = [&](auto t) {
+        using T = decltype(t);
+        if (m <= 16 || tiles(16) <= 512) return launch_small<T, SmallShape<1, 1, 8>>(what, ka, kb, m, n, nb, out, ld, stream);
+        if (tiles(32) <= 512 || !offsets) return launch_small<T, SmallShape<2, 2, 8>>(what, ka, kb, m, n, nb, out, ld, stream);
+        if (tiles(256) <= 128) return launch_big<T, BigShape<128, 128, 2, 2>>(what, ka, kb, m, n, nb, out, ld, stream);
+        return launch_big<T, BigShape<256, 256, 4, 2>>(what, ka, kb, m, n, nb, out, ld, stream);
+    };
+    return dtype == FS_BF16 ? go(uint16_t{}) : go(float{});
 }

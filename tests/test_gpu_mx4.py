@@ -311,7 +311,8 @@ def _check_product(a, b, out, m, n, k):
 
 MNK = [(1, 1, 1), (1, 1, 32), (1, 17, 33), (2, 16, 64), (16, 16, 128), (17, 15, 127), (15, 33, 129), (1, 300, 1000), (33, 64, 160),
        (64, 64, 256), (65, 63, 257), (100, 1, 4000), (128, 128, 512), (127, 129, 480), (130, 260, 1376), (256, 256, 256),
-       (257, 300, 1024), (8, 2048, 2048), (3, 1000, 5000), (300, 520, 2080), (512, 256, 130), (31, 96, 7000)]
+       (257, 300, 1024), (8, 2048, 2048), (3, 1000, 5000), (300, 520, 2080), (512, 256, 130), (31, 96, 7000),
+       (900, 1000, 1), (1000, 900, 33), (700, 1100, 480), (1300, 700, 481), (600, 2000, 545), (2500, 3000, 100), (2700, 3100, 700)]
 
 
 @pytest.mark.parametrize("m,n,k", MNK)
@@ -358,7 +359,30 @@ def test_matmul_with_strides_and_chunks(m, n, k):
         _check_product(b, a, outt, n, m, k)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 64, 128), (20, 40, 96), (256, 512, 512), (300, 300, 300)])
+@pytest.mark.parametrize("m,n,k,chunk,stride", [(200, 600, 512, 300, 600 << 20), (2048, 2100, 256, 700, 3 << 30), (3, 600, 512, 300, 3 << 30)])
+def test_matmul_with_chunks_far_apart(m, n, k, chunk, stride):
+    """Offsets past 31 and 32 bits."""
+    a, b = _random_matrix(m, k, 1), _random_matrix(n, k, 2)
+    nb, count = k // 32, -(-n // chunk)
+    buf = torch.empty((count - 1) * stride + chunk * 17 * nb, dtype=torch.uint8, device="cuda")
+    for c in range(count):
+        cc, ss = b[0][c * chunk:(c + 1) * chunk], b[1][c * chunk:(c + 1) * chunk]
+        at = c * stride
+        buf[at:at + cc.numel()] = cc.reshape(-1)
+        buf[at + chunk * 16 * nb:at + chunk * 16 * nb + ss.numel()] = ss.reshape(-1)
+    st = fs.Mx4MatrixStruct(buf.data_ptr(), buf.data_ptr() + chunk * 16 * nb, n, k, 16 * nb, nb, chunk, stride)
+    out, outt = torch.empty(m, n, device="cuda"), torch.empty(n, m, device="cuda")
+    say("far chunks", m, n, k)
+    fs.fs_mx4_matmul(fs.Mx4Matrix(*a, k), fs.Mx4Matrix._gathered(st, buf), out)
+    _check_product(a, b, out, m, n, k)
+    fs.fs_mx4_matmul(fs.Mx4Matrix._gathered(st, buf), fs.Mx4Matrix(*a, k), outt)
+    _check_product(b, a, outt, n, m, k)
+    w = torch.empty(n, k, dtype=torch.bfloat16, device="cuda")
+    fs.fs_mx4_dequantize(fs.Mx4Matrix._gathered(st, buf), w)
+    assert torch.equal(w.cpu().double(), torch.from_numpy(_decoded(*b, k)))
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 64, 128), (20, 40, 96), (256, 512, 512), (300, 300, 300), (2100, 2300, 400), (600, 700, 97)])
 def test_matmul_special_scales(m, n, k):
     a, b = _random_matrix(m, k, 3), _random_matrix(n, k, 4)
     a[1][m - 1, -1] = 255                                # NaN in a's last row
