@@ -106,10 +106,9 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
     if (STOCHASTIC && e >= 2 && (amax & 0x7FFFFFu) > 0x400000u) ++s;
     return s;
 }
-// 2^(s - 127); NaN for 255.
-__device__ __forceinline__ float scale_value(uint32_t s) {
-    return __uint_as_float(s == 0 ? 0x00400000u : s == 255 ? 0x7FC00000u : s << 23);
-}
+// 2^(s - 127).  For 255 the infinity's bits: the conversions go by the
+// exponent alone, and give NaN for every code.
+__device__ __forceinline__ float scale_value(uint32_t s) { return __uint_as_float(max(s << 23, 0x00400000u)); }
 
 // (a copy first: a bit cast of a vector's element takes the vector's first)
 __device__ __forceinline__ bf16x2 bf16_pair(const u32x4 &v, int k) {
