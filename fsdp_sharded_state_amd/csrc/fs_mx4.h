@@ -155,39 +155,69 @@ __device__ __forceinline__ Random8 philox8(uint64_t seed, uint64_t group, uint32
     return Random8{{c0, c1, c2, c3}};
 }
 
-// The code of |x| = y * 2^(s-127), y <= 6, rounded up where the fraction f of
-// the step above the code at or below y exceeds (r + 0.5) / 65536.  From 1 on
-// a step is half the value's binade: the code is the exponent and the top
-// mantissa bit, f the 22 bits under it.  Below 1 the step is 0.5.  All of it is exact.
-__device__ __forceinline__ uint32_t encode_up(float y, uint32_t r) {
-    const uint32_t b = __float_as_uint(y);
-    const bool one = b >= 0x3F800000u, half = b >= 0x3F000000u;
-    const uint32_t code = one ? (b >> 22) - (0x3F800000u >> 22) + 2 : half;
-    const float f = one ? (float)(b & 0x3FFFFFu) * 0x1p-22f : 2 * y - (half ? 1.0f : 0.0f);
-    return code + (f > fmaf((float)r, 0x1p-16f, 0x1p-17f));
-}
-template <class R>
-__device__ __forceinline__ uint32_t encode_stochastic(const R &r, uint32_t s, const Random8 &rnd) {
+// Stochastic codes of 8 elements: with y = |x| / 2^(s-127) <= 6, P the power
+// of two at or below y but at least 1, and P/2 the step of y's codes, y goes
+// up from the code at or below it where the fraction f of the step exceeds
+// t = (r + 0.5) / 65536.  The instruction that rounds to nearest then makes the code.
+//
+// bf16: it is given y + (0.5 - t) * P/2, which it rounds up where f > t.  y
+// has 8 significant bits and (0.5 - t) * P/2 is a multiple of P * 2^-18, so the
+// sum is exact from y = 2^-18 on, and below that f < 2^-17 <= t: the sum, at
+// most 0.25, goes down.  A tie, f = t, needs as many fraction bits as t has, which y has only below
+// 0.5: there the even code, zero, is the lower one.  The sum may lie under the power of two
+// at or below y, where the codes are denser: then that power is given, which is no more
+// than the code at or below y, or rounds down to it.
+__device__ __forceinline__ float power_below(float y) { return __uint_as_float(__float_as_uint(y) & 0x7F800000u); }
+__device__ __forceinline__ float with_sign(float y, float x) { return __builtin_copysignf(y, x); }
+
+__device__ __forceinline__ uint32_t encode_stochastic(const Raw8<uint16_t> &r, uint32_t s, const Random8 &rnd) {
     const float inv = __uint_as_float((254 - s) << 23);   // s <= 253
-    uint32_t c = 0;
+    float z[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const uint32_t b = __float_as_uint(elem(r, k));
-        const float y = __uint_as_float(b & 0x7FFFFFFFu) * inv;
-        const uint32_t u = k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu;
-        c |= (encode_up(y, u) | (b >> 31 << 3)) << (4 * k);
+        const float x = elem(r, k), y = fabsf(x) * inv;
+        const float u = (float)(k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu);
+        const float q = power_below(y);
+        z[k] = with_sign(fmaxf(fmaf(fmaxf(q, 1.f), fmaf(u, -0x1p-17f, 0.25f - 0x1p-18f), y), q), x);
     }
-    return c;
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[0], z[1], 1.f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[2], z[3], 1.f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[4], z[5], 1.f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[6], z[7], 1.f, 3);
+}
+// fp32: y / (P/2) is exact, so are its whole part and its fraction; the whole
+// part, one more where f > t, times P is twice the code's value.
+__device__ __forceinline__ uint32_t encode_stochastic(const Raw8<float> &r, uint32_t s, const Random8 &rnd) {
+    const float inv = __uint_as_float((254 - s) << 23);
+    float z[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float x = elem(r, k), y = fabsf(x) * inv, p = fmaxf(power_below(y), 1.f);
+        const float steps = y * __uint_as_float(0x7F800000u - __float_as_uint(p)), f = __builtin_amdgcn_fractf(steps);
+        const float u = (float)(k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu);
+        z[k] = with_sign((steps - f + (f > fmaf(u, 0x1p-16f, 0x1p-17f) ? 1.f : 0.f)) * p, x);
+    }
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[0], z[1], 2.f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[2], z[3], 2.f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[4], z[5], 2.f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[6], z[7], 2.f, 3);
 }
 
-// Codes and scale byte of a quad's block, from its lanes' quarters.  `group`:
-// 4 * block + the lane's quarter, for the random bits.
+// Codes of 8 elements of a block with scale byte s.  `group`: 4 * block + which
+// quarter they are, for the random bits.
+template <bool STOCHASTIC, class R>
+__device__ __forceinline__ uint32_t encode8_at(const R &r, uint32_t s, uint64_t seed, uint64_t group, uint32_t orientation) {
+    if (s == 255) return 0;
+    if (STOCHASTIC) return encode_stochastic(r, s, philox8(seed, group, orientation));
+    return encode_nearest(r, scale_value(s));
+}
+// The same and the scale byte, for a quad's block, each lane with its quarter.
 template <bool STOCHASTIC, class R>
 __device__ __forceinline__ uint32_t encode8(const R &r, uint64_t seed, uint64_t group, uint32_t orientation, uint32_t *s) {
     *s = scale_byte<STOCHASTIC>(quad_max(amax8(r)));
-    if (*s == 255) return 0;
-    if (STOCHASTIC) return encode_stochastic(r, *s, philox8(seed, group, orientation));
-    return encode_nearest(r, scale_value(*s));
+    return encode8_at<STOCHASTIC>(r, *s, seed, group, orientation);
 }
 
 __device__ __forceinline__ void decode8(float *v, uint32_t c, float scale) {

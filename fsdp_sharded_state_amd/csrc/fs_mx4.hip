@@ -163,80 +163,130 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
 
 // ---------------------------------------------------------------- matrices --
 
-constexpr int kMatTile = 128;                                  // rows and columns of a tile
-constexpr int kMatQuarters = kMatTile / 8;                     // lanes' quarters along it
-constexpr int kMatSteps = kMatTile * kMatQuarters / kThreads;
-
 struct Mx4Out {
     uint8_t *codes, *scales;
     int64_t code_stride, scale_stride;
 };
 
-// One tile: its rows' blocks straight from the loads, its columns' from a copy in LDS.
-template <class T, bool ROWS, bool COLS, bool STOCHASTIC>
-__global__ __launch_bounds__(kThreads) void quantize_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
-                                                                int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
-                                                                Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
-    constexpr int kPitch = kMatTile + 2;
-    __shared__ T lds[COLS ? kMatTile * kPitch : 1];
-    const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kMatTile, c0 = (int64_t)(blockIdx.x % tiles_x) * kMatTile;
-    const uint64_t seed = STOCHASTIC ? *seed_at : 0;
-    const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
-#pragma unroll
-    for (int i = 0; i < kMatSteps; ++i) {
-        const int q = i * kThreads + threadIdx.x, lr = q / kMatQuarters, lq = q % kMatQuarters;
-        const int64_t r = r0 + lr, c = c0 + 8 * lq;
-        Raw8<T> v;
-        load8(v, x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
-        if (ROWS) {
-            const int64_t b = c / kMx4Block;
-            uint32_t s;
-            const uint32_t code = encode8<STOCHASTIC>(v, seed, 4 * (uint64_t)(r * nbr + b) + (lq & 3), 0, &s);
-            if (r < rows && b < nbr) {
-                *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
-                if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
-            }
-        }
-        if (COLS) {
-            T e[8];
-            __builtin_memcpy(e, &v, sizeof e);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) lds[lr * kPitch + 8 * lq + k] = e[k];
-        }
-    }
-    if (!COLS) return;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kMatSteps; ++i) {
-        const int q = i * kThreads + threadIdx.x, lc = q / kMatQuarters, lq = q % kMatQuarters;
-        const int64_t c = c0 + lc, b = r0 / kMx4Block + lq / 4;
-        T e[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) e[k] = lds[(8 * lq + k) * kPitch + lc];
-        Raw8<T> v;
-        __builtin_memcpy(&v, e, sizeof v);
-        uint32_t s;
-        const uint32_t code = encode8<STOCHASTIC>(v, seed, 4 * (uint64_t)(c * nbc + b) + (lq & 3), 1, &s);
-        if (c < cols && b < nbc) {
-            *reinterpret_cast<uint32_t *>(by_col.codes + c * by_col.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
-            if ((lq & 3) == 0) by_col.scales[c * by_col.scale_stride + b] = (uint8_t)s;
-        }
-    }
+// Along rows alone, and back: a workgroup takes 16 rows by 128 elements, a lane 8 of them.
+constexpr int kRowTileCols = 128, kRowTileRows = kThreads * 8 / kRowTileCols;
+
+template <class T, bool STOCHASTIC>
+__global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
+                                                                     int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
+                                                                     const uint64_t *__restrict__ seed_at) {
+    const int lq = threadIdx.x % (kRowTileCols / 8);
+    const int64_t r = (int64_t)(blockIdx.x / tiles_x) * kRowTileRows + threadIdx.x / (kRowTileCols / 8);
+    const int64_t c = (int64_t)(blockIdx.x % tiles_x) * kRowTileCols + 8 * lq, b = c / kMx4Block;
+    const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
+    if (r >= rows || b >= nb) return;   // whole quads
+    Raw8<T> v;
+    load8(v, x + r * ldx + c, (int)imax(0, imin(8, cols - c)));
+    uint32_t s;
+    const uint32_t code = encode8<STOCHASTIC>(v, STOCHASTIC ? *seed_at : 0, 4 * (uint64_t)(r * nb + b) + (lq & 3), 0, &s);
+    *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
+    if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
 }
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
                                                                   int64_t ldo, uint32_t tiles_x) {
-    const int64_t r0 = (int64_t)(blockIdx.x / tiles_x) * kMatTile, c0 = (int64_t)(blockIdx.x % tiles_x) * kMatTile;
+    const int64_t r = (int64_t)(blockIdx.x / tiles_x) * kRowTileRows + threadIdx.x / (kRowTileCols / 8);
+    const int64_t c = (int64_t)(blockIdx.x % tiles_x) * kRowTileCols + 8 * (threadIdx.x % (kRowTileCols / 8));
+    if (r >= rows || c >= cols) return;
+    int64_t code, scale;
+    m.row((uint32_t)r, &code, &scale);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
+    store8(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
+}
+
+// Along columns, with or without rows: a workgroup takes 128 by 128 elements.
+// Its rows' blocks come straight from the loads, as above.  Its columns' come from a copy in
+// LDS, where a lane takes 32 rows of two columns (of one in fp32), two blocks of its own: reads
+// of whole rows by the wave, and no joins between lanes.
+constexpr int kColTile = 128, kColLanes = kColTile / 8, kColSteps = kColTile * kColLanes / kThreads;
+
+// The blocks in column `at` of a wave's 32 rows of LDS words: one for fp32, two for bf16.
+__device__ __forceinline__ void column_raws(Raw8<float> (&v)[1][4], const uint32_t *w) {
 #pragma unroll
-    for (int i = 0; i < kMatSteps; ++i) {
+    for (int k = 0; k < 8; ++k) v[0][k >> 1].v[k & 1] = u32x4{w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]};
+}
+__device__ __forceinline__ void column_raws(Raw8<uint16_t> (&v)[2][4], const uint32_t *w) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // the low halves of two rows, and the high ones
+            lo[i] = __builtin_amdgcn_perm(w[8 * k + 2 * i + 1], w[8 * k + 2 * i], 0x05040100);
+            hi[i] = __builtin_amdgcn_perm(w[8 * k + 2 * i + 1], w[8 * k + 2 * i], 0x07060302);
+        }
+        v[0][k].v = u32x4{lo[0], lo[1], lo[2], lo[3]};
+        v[1][k].v = u32x4{hi[0], hi[1], hi[2], hi[3]};
+    }
+}
+
+template <class T, bool ROWS, bool STOCHASTIC>
+__global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
+                                                                     int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
+                                                                     Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
+    constexpr int kPitch = kColTile * sizeof(T) + 16;   // bytes: the writes of 16 bytes by 16 lanes a row go on evenly over the banks
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kColTile * kPitch];
+    // neighbours share the cache lines of codes that they write: a run of tiles to each XCD
+    const uint32_t each = gridDim.x / kXcds, rest = gridDim.x % kXcds, xcd = blockIdx.x % kXcds;
+    const uint32_t id = xcd * each + min(xcd, rest) + blockIdx.x / kXcds;
+    const int64_t r0 = (int64_t)(id / tiles_x) * kColTile, c0 = (int64_t)(id % tiles_x) * kColTile;
+    const uint64_t seed = STOCHASTIC ? *seed_at : 0;
+    const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
+    Raw8<T> v[kColSteps];
+#pragma unroll
+    for (int i = 0; i < kColSteps; ++i) {
         const int q = i * kThreads + threadIdx.x;
-        const int64_t r = r0 + q / kMatQuarters, c = c0 + 8 * (q % kMatQuarters);
-        if (r >= rows || c >= cols) continue;
-        int64_t code, scale;
-        m.row((uint32_t)r, &code, &scale);
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
-        store8(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
+        const int64_t r = r0 + q / kColLanes, c = c0 + 8 * (q % kColLanes);
+        load8(v[i], x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kColSteps; ++i) {
+        const int q = i * kThreads + threadIdx.x, lr = q / kColLanes, lq = q % kColLanes;
+        __builtin_memcpy(__builtin_assume_aligned(lds + lr * kPitch + lq * sizeof v[i], 16), &v[i], sizeof v[i]);
+    }
+    if (ROWS) {
+#pragma unroll
+        for (int i = 0; i < kColSteps; ++i) {
+            const int q = i * kThreads + threadIdx.x, lq = q % kColLanes;
+            const int64_t r = r0 + q / kColLanes, b = c0 / kMx4Block + lq / 4;
+            uint32_t s;
+            const uint32_t code = encode8<STOCHASTIC>(v[i], seed, 4 * (uint64_t)(r * nbr + b) + (lq & 3), 0, &s);
+            if (r < rows && b < nbr) {
+                *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
+                if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
+            }
+        }
+    }
+    __syncthreads();
+    constexpr int kWide = 4 / sizeof(T), kWords = kColTile / kWide;   // columns a lane, lanes a row
+    constexpr int kItems = kWords * (kColTile / kMx4Block) / kThreads;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int q = i * kThreads + threadIdx.x, lb = q / kWords, lc = q % kWords;
+        const int64_t b = r0 / kMx4Block + lb;
+        if (b >= nbc) continue;
+        uint32_t w[kMx4Block];
+#pragma unroll
+        for (int k = 0; k < kMx4Block; ++k) w[k] = *reinterpret_cast<const uint32_t *>(lds + (lb * kMx4Block + k) * kPitch + lc * 4);
+        Raw8<T> e[kWide][4];
+        column_raws(e, w);
+#pragma unroll
+        for (int j = 0; j < kWide; ++j) {
+            const int64_t c = c0 + lc * kWide + j;
+            const uint32_t s = scale_byte<STOCHASTIC>(max(max(amax8(e[j][0]), amax8(e[j][1])), max(amax8(e[j][2]), amax8(e[j][3]))));
+            uint32_t code[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) code[k] = encode8_at<STOCHASTIC>(e[j][k], s, seed, 4 * (uint64_t)(c * nbc + b) + k, 1);
+            if (c < cols) {
+                *reinterpret_cast<u32x4 *>(by_col.codes + c * by_col.code_stride + b * kMx4BlockBytes) = u32x4{code[0], code[1], code[2], code[3]};
+                by_col.scales[c * by_col.scale_stride + b] = (uint8_t)s;
+            }
+        }
     }
 }
 
@@ -500,8 +550,8 @@ int check_plain(const char *what, const char *name, const void *p, int64_t rows,
     return FS_OK;
 }
 
-int mat_tiles(const char *what, int64_t rows, int64_t cols, uint32_t *across, uint32_t *tiles) {
-    const int64_t x = (cols + kMatTile - 1) / kMatTile, y = (rows + kMatTile - 1) / kMatTile;
+int mat_tiles(const char *what, int64_t rows, int64_t cols, int64_t tile_rows, int64_t tile_cols, uint32_t *across, uint32_t *tiles) {
+    const int64_t x = (cols + tile_cols - 1) / tile_cols, y = (rows + tile_rows - 1) / tile_rows;
     if (x * y > kMaxGrid) return fail(FS_E_OVERFLOW, "%s: too large for one launch", what);
     *across = (uint32_t)x;
     *tiles = (uint32_t)(x * y);
@@ -530,7 +580,9 @@ extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dty
     if (by_col)
         if (int rc = check_out(what, "by_col", by_col, cols, rows, &col, spans, &count)) return rc;
     uint32_t across, tiles;
-    if (int rc = mat_tiles(what, rows, cols, &across, &tiles)) return rc;
+    if (int rc = by_col ? mat_tiles(what, rows, cols, kColTile, kColTile, &across, &tiles)
+                        : mat_tiles(what, rows, cols, kRowTileRows, kRowTileCols, &across, &tiles))
+        return rc;
     if (tiles == 0) return FS_OK;
     (void)hipGetLastError();
     by_type(dtype, seed != nullptr, [&](auto t, auto stochastic) {
@@ -538,15 +590,15 @@ extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dty
         constexpr bool S = decltype(stochastic)::value;
         const T *src = static_cast<const T *>(x);
         const int64_t ld = rows > 1 ? ldx : 0;
-        if (by_row && by_col)
-            hipLaunchKernelGGL((quantize_mx4_kernel<T, true, true, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
-                               cols, src, ld, across, row, col, seed);
+        if (!by_col)
+            hipLaunchKernelGGL((quantize_rows_mx4_kernel<T, S>), dim3(tiles), dim3(kThreads), 0, stream, rows, cols, src, ld,
+                               across, row, seed);
         else if (by_row)
-            hipLaunchKernelGGL((quantize_mx4_kernel<T, true, false, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
-                               cols, src, ld, across, row, col, seed);
+            hipLaunchKernelGGL((quantize_cols_mx4_kernel<T, true, S>), dim3(tiles), dim3(kThreads), 0, stream, rows, cols,
+                               src, ld, across, row, col, seed);
         else
-            hipLaunchKernelGGL((quantize_mx4_kernel<T, false, true, S>), dim3(tiles), dim3(kThreads), 0, stream, rows,
-                               cols, src, ld, across, row, col, seed);
+            hipLaunchKernelGGL((quantize_cols_mx4_kernel<T, false, S>), dim3(tiles), dim3(kThreads), 0, stream, rows, cols,
+                               src, ld, across, row, col, seed);
     });
     return check_launch(what);
 }
@@ -563,7 +615,7 @@ extern "C" int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype d
     if (ranges_overlap(out, span, k.codes, code_span) || ranges_overlap(out, span, k.scales, scale_span))
         return fail(FS_E_INVAL, "%s: out overlaps the matrix", what);
     uint32_t across, tiles;
-    if (int rc = mat_tiles(what, m->rows, m->cols, &across, &tiles)) return rc;
+    if (int rc = mat_tiles(what, m->rows, m->cols, kRowTileRows, kRowTileCols, &across, &tiles)) return rc;
     if (tiles == 0) return FS_OK;
     (void)hipGetLastError();
     by_type(dtype, false, [&](auto t, auto) {
