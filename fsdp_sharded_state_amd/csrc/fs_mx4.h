@@ -9,6 +9,8 @@
 // scale, fp32 values on and beside every midpoint, and every code at every
 // scale): 4 instructions a lane, so the conversions stay under the HBM time.
 #pragma once
+#include <type_traits>
+
 #include "fs_device.h"
 #include "fs_mx4_plan.h"
 
@@ -18,14 +20,44 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// 16 bytes at any element-aligned address: the target allows unaligned
-// vector accesses, and memcpy tells the compiler that this is one.
-__device__ __forceinline__ u32x4 ld16_any(const void *p) {
-    u32x4 v;
-    __builtin_memcpy(&v, p, 16);
-    return v;
+// Accesses to global memory through any pointer.  Where the pointer was itself
+// read from memory the compiler would take the generic ones, which are slower: the copy-out
+// of 45M fp32 elements to odd addresses took 46 us with those, 34 with these.
+template <class T>
+using Global = __attribute__((address_space(1))) T;
+template <class T>
+__device__ __forceinline__ T ld(const T *p) {
+    return *(const Global<T> *)reinterpret_cast<uintptr_t>(p);
 }
-__device__ __forceinline__ void st16_any(void *p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+template <class T>
+__device__ __forceinline__ void st(T *p, T v) {
+    *(Global<T> *)reinterpret_cast<uintptr_t>(p) = v;
+}
+// 16 bytes at any element-aligned address: the target allows unaligned vector accesses.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+__device__ __forceinline__ u32x4 ld16_any(const void *p) { return *(const Global<u32x4_any> *)reinterpret_cast<uintptr_t>(p); }
+__device__ __forceinline__ void st16_any(void *p, u32x4 v) { *(Global<u32x4_any> *)reinterpret_cast<uintptr_t>(p) = v; }
+// Past the caches, on 16 bytes.  Elements pass through once, and what a call
+// leaves in the caches to be written back costs the next one: copy-in and copy-out of one 7B block
+// in bf16 take 206 us without, 156 with.  Off 16 bytes lanes share sectors, which the caches have to join, and so it is
+// with the two pieces of 8 fp32 values (copy-out of 45M: 34 us through the caches, 84 past them).
+// The two kinds of access are chosen by a template argument: the compiler makes one of a choice beside them.
+template <bool PAST>
+__device__ __forceinline__ u32x4 ld16_el(const void *p) {
+    if (PAST) return __builtin_nontemporal_load((const Global<u32x4> *)reinterpret_cast<uintptr_t>(p));
+    return ld16_any(p);
+}
+template <bool PAST>
+__device__ __forceinline__ void st16_el(void *p, u32x4 v) {
+    if (PAST) __builtin_nontemporal_store(v, (Global<u32x4> *)reinterpret_cast<uintptr_t>(p));
+    else st16_any(p, v);
+}
+// f(std::bool_constant<past>())
+template <class F>
+__device__ __forceinline__ void with_past(bool past, F &&f) {
+    if (past) f(std::true_type{});
+    else f(std::false_type{});
+}
 
 // Eight elements of either type as they lie in memory.
 template <class T>
@@ -39,28 +71,32 @@ struct Raw8<float> {
     u32x4 v[2];
 };
 
+__device__ __forceinline__ bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // `valid` (any value) elements from p on, zeros after them.
+template <bool PAST>
 __device__ __forceinline__ void load8(Raw8<uint16_t> &r, const uint16_t *p, int valid) {
     if (valid >= 8) {
-        r.v = ld16_any(p);
+        r.v = ld16_el<PAST>(p);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = 2 * k < valid ? p[2 * k] : 0, hi = 2 * k + 1 < valid ? p[2 * k + 1] : 0;
+            const uint32_t lo = 2 * k < valid ? ld(p + 2 * k) : 0, hi = 2 * k + 1 < valid ? ld(p + 2 * k + 1) : 0;
             w[k] = lo | (hi << 16);
         }
         r.v = u32x4{w[0], w[1], w[2], w[3]};
     }
 }
+template <bool PAST>
 __device__ __forceinline__ void load8(Raw8<float> &r, const float *p, int valid) {
     if (valid >= 8) {
-        r.v[0] = ld16_any(p);
-        r.v[1] = ld16_any(p + 4);
+        r.v[0] = ld16_el<PAST>(p);
+        r.v[1] = ld16_el<PAST>(p + 4);
     } else {
         uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = k < valid ? __float_as_uint(p[k]) : 0u;
+        for (int k = 0; k < 8; ++k) w[k] = k < valid ? __float_as_uint(ld(p + k)) : 0u;
         r.v[0] = u32x4{w[0], w[1], w[2], w[3]};
         r.v[1] = u32x4{w[4], w[5], w[6], w[7]};
     }
@@ -133,6 +169,10 @@ __device__ __forceinline__ uint32_t encode_nearest(const Raw8<float> &r, float s
     return c;
 }
 
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+    return (uint32_t)__builtin_amdgcn_bitop3_b32((int)a, (int)b, (int)c, 0x96);   // the truth table of a ^ b ^ c
+}
+
 struct Random8 {
     uint32_t w[4];
 };
@@ -145,9 +185,9 @@ __device__ __forceinline__ Random8 philox8(uint64_t seed, uint64_t group, uint32
 #pragma unroll
     for (int i = 0; i < 7; ++i) {
         const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
-        c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+        c0 = xor3((uint32_t)(p1 >> 32), c1, k0);
         c1 = (uint32_t)p1;
-        c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+        c2 = xor3((uint32_t)(p0 >> 32), c3, k1);
         c3 = (uint32_t)p0;
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
@@ -168,6 +208,10 @@ __device__ __forceinline__ Random8 philox8(uint64_t seed, uint64_t group, uint32
 // at or below y, where the codes are denser: then that power is given, which is no more
 // than the code at or below y, or rounds down to it.
 __device__ __forceinline__ float power_below(float y) { return __uint_as_float(__float_as_uint(y) & 0x7F800000u); }
+// The larger of two values, of which b is not negative: as integers, which need no care for NaN.
+__device__ __forceinline__ float larger(float a, float b) {
+    return __uint_as_float((uint32_t)max((int)__float_as_uint(a), (int)__float_as_uint(b)));
+}
 __device__ __forceinline__ float with_sign(float y, float x) { return __builtin_copysignf(y, x); }
 
 __device__ __forceinline__ uint32_t encode_stochastic(const Raw8<uint16_t> &r, uint32_t s, const Random8 &rnd) {
@@ -178,7 +222,7 @@ __device__ __forceinline__ uint32_t encode_stochastic(const Raw8<uint16_t> &r, u
         const float x = elem(r, k), y = fabsf(x) * inv;
         const float u = (float)(k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu);
         const float q = power_below(y);
-        z[k] = with_sign(fmaxf(fmaf(fmaxf(q, 1.f), fmaf(u, -0x1p-17f, 0.25f - 0x1p-18f), y), q), x);
+        z[k] = with_sign(larger(fmaf(larger(q, 1.f), fmaf(u, -0x1p-17f, 0.25f - 0x1p-18f), y), q), x);
     }
     uint32_t c = 0;
     c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, z[0], z[1], 1.f, 0);
@@ -193,7 +237,7 @@ __device__ __forceinline__ uint32_t encode_stochastic(const Raw8<float> &r, uint
     float z[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float x = elem(r, k), y = fabsf(x) * inv, p = fmaxf(power_below(y), 1.f);
+        const float x = elem(r, k), y = fabsf(x) * inv, p = larger(power_below(y), 1.f);
         const float steps = y * __uint_as_float(0x7F800000u - __float_as_uint(p)), f = __builtin_amdgcn_fractf(steps);
         const float u = (float)(k & 1 ? rnd.w[k >> 1] >> 16 : rnd.w[k >> 1] & 0xFFFFu);
         z[k] = with_sign((steps - f + (f > fmaf(u, 0x1p-16f, 0x1p-17f) ? 1.f : 0.f)) * p, x);
@@ -235,30 +279,35 @@ __device__ __forceinline__ u32x4 decode8_bf16(uint32_t c, float scale) {
 }
 
 // The first `valid` of the 8 values of codes c to p.
+template <bool PAST>
 __device__ __forceinline__ void store8(uint16_t *p, uint32_t c, float scale, int valid) {
     const u32x4 v = decode8_bf16(c, scale);
     if (valid >= 8) {
-        st16_any(p, v);
+        st16_el<PAST>(p, v);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < valid) p[k] = (uint16_t)(word(v, k >> 1) >> (16 * (k & 1)));
+            if (k < valid) st(p + k, (uint16_t)(word(v, k >> 1) >> (16 * (k & 1))));
     }
 }
+template <bool PAST>
 __device__ __forceinline__ void store8(float *p, const float *v, int valid) {
     if (valid >= 8) {
-        __builtin_memcpy(p, v, 16);
-        __builtin_memcpy(p + 4, v + 4, 16);
+        u32x4 w[2];
+        __builtin_memcpy(w, v, sizeof w);
+        st16_el<PAST>(p, w[0]);
+        st16_el<PAST>(p + 4, w[1]);
     } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            if (k < valid) p[k] = v[k];
+            if (k < valid) st(p + k, v[k]);
     }
 }
+template <bool PAST>
 __device__ __forceinline__ void store8(float *p, uint32_t c, float scale, int valid) {
     float v[8];
     decode8(v, c, scale);
-    store8(p, v, valid);
+    store8<PAST>(p, v, valid);
 }
 
 // A matrix of blocks, by value.  Rows fit in 31 bits, so a row's chunk comes

@@ -15,6 +15,8 @@ static_assert(kTileSteps * kQuads == kMx4TileBlocks, "a tile is whole steps");
 
 // ------------------------------------------------------------------ shards --
 
+// A tile's codes and scales go through LDS: 16 bytes a lane are stored for the
+// four that a lane makes at a time, and four scales for one.
 template <class T, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
                                                             const Mx4Run *__restrict__ pads,
@@ -22,6 +24,8 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
                                                             uint8_t *__restrict__ out, int32_t first_rank,
                                                             int64_t shard_blocks, int64_t shard_bytes,
                                                             const uint64_t *__restrict__ seed_at) {
+    __shared__ uint32_t lds_codes[kMx4TileBlocks * 4];
+    __shared__ __attribute__((aligned(4))) uint8_t lds_scales[kMx4TileBlocks];
     const int tid = threadIdx.x;
     if (blockIdx.x >= ntiles) {   // blocks of no piece, or the bytes after the last scale
         const Mx4Run run = pads[blockIdx.x - ntiles];
@@ -37,27 +41,30 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
     }
     const Mx4Tile t = tiles[blockIdx.x];
     const T *src = static_cast<const T *>(params[t.param]) + t.src;
-    uint8_t *shard = out + (t.rank - first_rank) * shard_bytes;
-    uint32_t *codes = reinterpret_cast<uint32_t *>(shard + t.blk * kMx4BlockBytes);
-    uint8_t *scales = shard + shard_blocks * kMx4BlockBytes + t.blk;
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const uint64_t group = 4 * (uint64_t)(t.rank * shard_blocks + t.blk);
     Raw8<T> r[kTileSteps];
+    with_past(on16(src), [&](auto past) {
 #pragma unroll
-    for (int i = 0; i < kTileSteps; ++i) {
-        const int q = i * kThreads + tid;
-        load8(r[i], src + 8 * q, t.n - 8 * q);
-    }
+        for (int i = 0; i < kTileSteps; ++i) {
+            const int q = i * kThreads + tid;
+            load8<past>(r[i], src + 8 * q, t.n - 8 * q);
+        }
+    });
 #pragma unroll
     for (int i = 0; i < kTileSteps; ++i) {
         const int q = i * kThreads + tid;
         uint32_t s;
-        const uint32_t c = encode8<STOCHASTIC>(r[i], seed, group + q, 0, &s);
-        if ((q >> 2) < t.nblk) {
-            codes[q] = c;
-            if ((tid & 3) == 0) scales[q >> 2] = (uint8_t)s;
-        }
+        lds_codes[q] = encode8<STOCHASTIC>(r[i], seed, group + q, 0, &s);
+        if ((tid & 3) == 0) lds_scales[q >> 2] = (uint8_t)s;
     }
+    __syncthreads();
+    uint8_t *shard = out + (t.rank - first_rank) * shard_bytes;
+    if (tid < t.nblk)
+        *reinterpret_cast<u32x4 *>(shard + (t.blk + tid) * kMx4BlockBytes) = *reinterpret_cast<const u32x4 *>(lds_codes + 4 * tid);
+    if (4 * tid < t.nblk)   // whole words: blocks come in eights
+        *reinterpret_cast<uint32_t *>(shard + shard_blocks * kMx4BlockBytes + t.blk + 4 * tid) =
+            *reinterpret_cast<const uint32_t *>(lds_scales + 4 * tid);
 }
 
 template <class T>
@@ -80,11 +87,26 @@ __global__ __launch_bounds__(kThreads) void unpack_mx4_kernel(const Mx4Tile *__r
             s[i] = scales[q >> 2];
         }
     }
+    with_past(sizeof(T) == 2 && on16(dst), [&](auto past) {
 #pragma unroll
-    for (int i = 0; i < kTileSteps; ++i) {
-        const int q = i * kThreads + tid;
-        if (8 * q < t.n) store8(dst + 8 * q, c[i], scale_value(s[i]), t.n - 8 * q);
-    }
+        for (int i = 0; i < kTileSteps; ++i) {
+            const int q = i * kThreads + tid;
+            if (8 * q < t.n) store8<past>(dst + 8 * q, c[i], scale_value(s[i]), t.n - 8 * q);
+        }
+    });
+}
+
+// In the reduce a workgroup takes one of kParts parts of a tile, so that a wave lives for
+// one round of loads and many are on a CU.  The parts share cache lines
+// of scales, and go to one XCD: eight tiles at a time, the last ones in turn.
+constexpr uint32_t kParts = kTileSteps, kXcds = 8;
+
+struct TilePart {
+    uint32_t tile, part;
+};
+__device__ __forceinline__ TilePart part_of(uint32_t id, uint32_t ntiles) {
+    if (id < ntiles / kXcds * kXcds * kParts) return {id / (kXcds * kParts) * kXcds + id % kXcds, id / kXcds % kParts};
+    return {id / kParts, id % kParts};
 }
 
 constexpr int kMx4Terms = 64;   // slices of one launch; the sums of more are carried through `out`
@@ -111,11 +133,9 @@ __device__ __forceinline__ void add_slices(float (&acc)[8], const Mx4Slices &sli
     }
 }
 
-// A workgroup takes a quarter of a tile, 8 elements a lane, so that a wave lives for one round of loads and many are on
-// a CU: 41.6 us for one 7B block's shard of 8 slices, 296 for three of 32, where whole tiles took 44.3 and 350, two steps at a
-// time 48 and 295, four 53 and 302.  The quarters of a tile share cache lines of scales and go to one
-// XCD, and whole pieces of 16 bytes are stored past the caches (40.6 and 282).
-constexpr uint32_t kParts = kTileSteps, kXcds = 8;
+// One 7B block's shard of 8 slices takes 41.6 us in parts of tiles, three of 32 slices 296, where whole tiles took 44.3 and
+// 350, two steps at a time 48 and 295, four 53 and 302.  With the parts of a tile on one XCD, and
+// stores past the caches, 40.6 and 282.
 
 __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
                                                               const Mx4Run *__restrict__ gaps, Mx4Slices slices,
@@ -128,11 +148,10 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
         for (int k = tid; k < run.n; k += kThreads) out[run.at + k] = 0.f;
         return;
     }
-    const bool even = id < ntiles / kXcds * kXcds * kParts;   // eight tiles at a time, the last ones in turn
-    const uint32_t part = even ? id / kXcds % kParts : id % kParts;
-    const Mx4Tile t = tiles[even ? id / (kXcds * kParts) * kXcds + id % kXcds : id / kParts];
-    if (part == 0 && tid < t.fill) out[t.elem + t.n + tid] = 0.f;
-    const int q = part * kThreads + tid, valid = t.n - 8 * q;
+    const TilePart at = part_of(id, ntiles);
+    const Mx4Tile t = tiles[at.tile];
+    if (at.part == 0 && tid < t.fill) out[t.elem + t.n + tid] = 0.f;
+    const int q = at.part * kThreads + tid, valid = t.n - 8 * q;
     if (valid <= 0) return;
     const int64_t code0 = t.blk * kMx4BlockBytes, scale0 = shard_blocks * kMx4BlockBytes + t.blk;
     float *dst = out + t.elem + 8 * q;
@@ -151,14 +170,7 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
     for (; j < nterms; ++j) add_slices<1>(acc, slices, j, code0, scale0, q);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = divide != 0.f ? acc[k] / divide : acc[k] * scale;
-    if (valid >= 8 && (reinterpret_cast<uintptr_t>(dst) & 15) == 0) {
-        u32x4 v[2];
-        __builtin_memcpy(v, acc, sizeof v);
-        st16(reinterpret_cast<char *>(dst), v[0]);
-        st16(reinterpret_cast<char *>(dst + 4), v[1]);
-    } else {
-        store8(dst, acc, valid);
-    }
+    with_past(on16(out + t.elem), [&](auto past) { store8<past>(dst, acc, valid); });
 }
 
 // ---------------------------------------------------------------- matrices --
@@ -181,7 +193,8 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t row
     const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
     if (r >= rows || b >= nb) return;   // whole quads
     Raw8<T> v;
-    load8(v, x + r * ldx + c, (int)imax(0, imin(8, cols - c)));
+    with_past(on16(x) && ldx * sizeof(T) % 16 == 0,
+              [&](auto past) { load8<past>(v, x + r * ldx + c, (int)imax(0, imin(8, cols - c))); });
     uint32_t s;
     const uint32_t code = encode8<STOCHASTIC>(v, STOCHASTIC ? *seed_at : 0, 4 * (uint64_t)(r * nb + b) + (lq & 3), 0, &s);
     *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
@@ -197,7 +210,9 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
     int64_t code, scale;
     m.row((uint32_t)r, &code, &scale);
     const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
-    store8(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
+    with_past(sizeof(T) == 2 && on16(out) && ldo * sizeof(T) % 16 == 0, [&](auto past) {
+        store8<past>(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
+    });
 }
 
 // Along columns, with or without rows: a workgroup takes 128 by 128 elements.
@@ -238,12 +253,14 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
     Raw8<T> v[kColSteps];
+    with_past(on16(x) && ldx * sizeof(T) % 16 == 0, [&](auto past) {
 #pragma unroll
-    for (int i = 0; i < kColSteps; ++i) {
-        const int q = i * kThreads + threadIdx.x;
-        const int64_t r = r0 + q / kColLanes, c = c0 + 8 * (q % kColLanes);
-        load8(v[i], x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
-    }
+        for (int i = 0; i < kColSteps; ++i) {
+            const int q = i * kThreads + threadIdx.x;
+            const int64_t r = r0 + q / kColLanes, c = c0 + 8 * (q % kColLanes);
+            load8<past>(v[i], x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
+        }
+    });
 #pragma unroll
     for (int i = 0; i < kColSteps; ++i) {
         const int q = i * kThreads + threadIdx.x, lr = q / kColLanes, lq = q % kColLanes;
