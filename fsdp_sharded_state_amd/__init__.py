@@ -135,8 +135,7 @@ def lib() -> ctypes.CDLL:
     mat = ctypes.POINTER(Mx4MatrixStruct)
     L.fs_mx4_quantize.argtypes = [i64, i64, vp, i32, i64, mat, mat, vp, vp]
     L.fs_mx4_dequantize.argtypes = [mat, vp, i32, i64, vp]
-    L.fs_mx4_matmul.argtypes = [mat, mat, vp, i32, i64, vp, sz, vp]
-    L.fs_mx4_matmul_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+    L.fs_mx4_matmul.argtypes = [mat, mat, vp, i32, i64, vp]
     L.fs_mx4_plan.argtypes = [vp, ctypes.POINTER(vp)]
     L.fs_mx4_plan_info.argtypes = [vp, ctypes.POINTER(Mx4PlanInfo)]
     L.fs_mx4_plan_piece.argtypes = [vp, i32, i32, ctypes.POINTER(i64), ctypes.POINTER(i64)]
@@ -158,7 +157,7 @@ def lib() -> ctypes.CDLL:
                  "fs_reshard_upload", "fs_reshard", "fs_load_local", "fs_reduce_adamw_step_noalloc",
                  "fs_grad_norm", "fs_grad_norm_workspace", "fs_clip_grads", "fs_reduce_shard_norm",
                  "fs_reduce_shard_norm_workspace", "fs_adamw_step_clip",
-                 "fs_mx4_quantize", "fs_mx4_dequantize", "fs_mx4_matmul", "fs_mx4_matmul_workspace", "fs_mx4_plan",
+                 "fs_mx4_quantize", "fs_mx4_dequantize", "fs_mx4_matmul", "fs_mx4_plan",
                  "fs_mx4_plan_info", "fs_mx4_plan_piece", "fs_mx4_plan_upload", "fs_mx4_plan_matrix", "fs_pack_mx4",
                  "fs_unpack_mx4", "fs_reduce_shard_mx4",
                  "fs_copy_bytes", "fs_stream_read", "fs_stream_fill"):
@@ -345,15 +344,19 @@ class Plan:
             raise ValueError(f"{what}: expected {self.info.n_params} tensors, got {len(tensors)}")
         esz = self.info.elem_bytes if elem_bytes is None else elem_bytes
         want = self.numels if numels is None else numels
-        ptrs = []
-        for i, t in enumerate(tensors):
-            if t.element_size() != esz:
-                raise ValueError(f"{what}[{i}]: element size {t.element_size()} != {esz}")
-            if t.numel() != want[i]:
-                raise ValueError(f"{what}[{i}]: numel {t.numel()} != {want[i]}")
-            ptrs.append(_dev_ptr(t, f"{what}[{i}]") if t.numel() else 0)
-        key = (tuple(ptrs), str(tensors[0].device) if tensors else "")
-        capturing = torch.cuda.is_available() and torch.cuda.is_current_stream_capturing()
+        ptrs = [t.data_ptr() if t.numel() else 0 for t in tensors]
+        if [t.numel() for t in tensors] != list(want) or not all(
+                t.element_size() == esz and t.is_cuda and t.is_contiguous() for t in tensors):
+            for i, t in enumerate(tensors):     # which one it is
+                if t.element_size() != esz:
+                    raise ValueError(f"{what}[{i}]: element size {t.element_size()} != {esz}")
+                if t.numel() != want[i]:
+                    raise ValueError(f"{what}[{i}]: numel {t.numel()} != {want[i]}")
+                if t.numel():
+                    _dev_ptr(t, f"{what}[{i}]")
+        key = (tuple(ptrs), tensors[0].get_device() if tensors else -1)
+        capturing = ((tensors and tensors[0].is_cuda or torch.cuda.is_available()) and
+                     torch.cuda.is_current_stream_capturing())
         tab = self._ptr_cache.get(key)
         if tab is None:
             if capturing:
@@ -845,7 +848,10 @@ class Mx4Matrix:
         self._hold(m, gathered.get_device(), (gathered,))
         return self
 
-    def _live(self):
+    def _on(self, index: int, name: str):
+        """The matrix for a call on GPU `index`."""
+        if self._index != index:
+            raise ValueError(f"{name} is on GPU {self._index}, the other arguments on cuda:{index}")
         for t, ptr in self._tensors:
             if t.data_ptr() != ptr:
                 raise ValueError("the matrix's tensors no longer have the memory they had when it was made")
@@ -859,23 +865,17 @@ def fs_mx4_empty(rows: int, cols: int, device="cuda") -> Mx4Matrix:
                      torch.empty(rows, nb, dtype=torch.uint8, device=device), cols)
 
 
-def _same_gpu(index: int, *named):
-    for name, other in named:
-        if other != index:
-            raise ValueError(f"{name} is on GPU {other}, the other arguments on cuda:{index}")
-
-
 def _plain_matrix(t: torch.Tensor, what: str) -> tuple:
-    """(address, dtype code, row stride) of a matrix whose rows are contiguous."""
-    code = _DTYPE_CODES.get(t.dtype)
+    """(rows, columns, address, dtype code, row stride, GPU) of a matrix whose rows are contiguous."""
+    code, index = _DTYPE_CODES.get(t.dtype), t.get_device()
     if code is None or t.dim() != 2:
         raise ValueError(f"{what} must be a bfloat16 or float32 matrix")
-    if not t.is_cuda:
+    if index < 0:
         raise ValueError(f"{what} must be a GPU tensor")
-    rows, cols = t.shape
-    if cols > 1 and rows and t.stride(1) != 1:
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1 and rows:
         raise ValueError(f"{what}: the elements of a row must follow each other")
-    return t.data_ptr(), code, t.stride(0)
+    return rows, cols, t.data_ptr(), code, ld, index
 
 
 def fs_mx4_quantize(x: torch.Tensor, by_row: Optional[Mx4Matrix] = None, by_col: Optional[Mx4Matrix] = None, *,
@@ -884,42 +884,31 @@ def fs_mx4_quantize(x: torch.Tensor, by_row: Optional[Mx4Matrix] = None, by_col:
     rows into by_row, along its columns into by_col (the transpose's shape),
     or both in one pass.  seed: None rounds to nearest; one int64 on the GPU
     rounds stochastically by it, read when the kernel runs."""
-    ptr, code, ld = _plain_matrix(x, "x")
-    index = x.get_device()
-    rows, cols = x.shape
-    for name, m in (("by_row", by_row), ("by_col", by_col)):
-        if m is not None:
-            _same_gpu(index, (name, m._index))
-    _launch(index, stream, lib().fs_mx4_quantize, rows, cols, ptr, code, ld,
-            None if by_row is None else by_row._live(), None if by_col is None else by_col._live(),
-            _scalar_ptr(seed, torch.int64, index, "seed"))
+    rows, cols, ptr, code, ld, index = _plain_matrix(x, "x")
+    row = col = None
+    if by_row is not None:
+        row = by_row._on(index, "by_row")
+    if by_col is not None:
+        col = by_col._on(index, "by_col")
+    _launch(index, stream, lib().fs_mx4_quantize, rows, cols, ptr, code, ld, row, col,
+            None if seed is None else _scalar_ptr(seed, torch.int64, index, "seed"))
 
 
 def fs_mx4_dequantize(m: Mx4Matrix, out: torch.Tensor, *, stream=None):
     """The values of a matrix of 4-bit blocks, as bf16 or fp32 (out's type)."""
-    ptr, code, ld = _plain_matrix(out, "out")
-    if tuple(out.shape) != m.shape:
+    rows, cols, ptr, code, ld, index = _plain_matrix(out, "out")
+    if (rows, cols) != m.shape:
         raise ValueError(f"fs_mx4_dequantize: out must be {m.shape}")
-    index = out.get_device()
-    _same_gpu(index, ("the matrix", m._index))
-    _launch(index, stream, lib().fs_mx4_dequantize, m._live(), ptr, code, ld)
+    _launch(index, stream, lib().fs_mx4_dequantize, m._on(index, "the matrix"), ptr, code, ld)
 
 
 def fs_mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor, *, stream=None):
     """out = a b^T (bf16 or fp32, any row stride): a is (m, k), b (n, k), out
-    (m, n).  Summed in fp32.  stream: a torch stream or a raw handle, which is
-    not to be destroyed before the call's work is done; not the per-thread
-    default stream."""
-    ptr, code, ld = _plain_matrix(out, "out")
-    m, k = a.shape
-    n = b.shape[0]
-    if b.shape[1] != k or tuple(out.shape) != (m, n):
+    (m, n).  Summed in fp32."""
+    m, n, ptr, code, ld, index = _plain_matrix(out, "out")
+    if a.shape[1] != b.shape[1] or a.shape[0] != m or b.shape[0] != n:
         raise ValueError(f"fs_mx4_matmul: a {a.shape} by b {b.shape} transposed does not give {tuple(out.shape)}")
-    index = out.get_device()
-    _same_gpu(index, ("a", a._index), ("b", b._index))
-    need = ctypes.c_int64()
-    _check(lib().fs_mx4_matmul_workspace(m, n, k, ctypes.byref(need)))
-    _launch(index, stream, lib().fs_mx4_matmul, a._live(), b._live(), ptr, code, ld, scratch=need.value)
+    _launch(index, stream, lib().fs_mx4_matmul, a._on(index, "a"), b._on(index, "b"), ptr, code, ld)
 
 
 class Mx4Plan:
@@ -973,13 +962,10 @@ class Mx4Plan:
     def _params(self, tensors, what: str, index: int, stream) -> tuple:
         if not tensors:
             return 0, FS_BF16
-        dt = tensors[0].dtype
-        for i, t in enumerate(tensors):
-            if t.dtype is not dt:
-                raise ValueError(f"{what} must share one dtype")
-            if t.get_device() != index:
-                raise ValueError(f"{what}[{i}] is on {t.device}, the buffer on cuda:{index}")
-        code = _dtype_code(dt)
+        kinds = {(t.dtype, t.get_device()) for t in tensors}
+        if len(kinds) > 1 or tensors[0].get_device() != index:
+            raise ValueError(f"{what} must share one dtype, on the buffer's GPU")
+        code = _dtype_code(tensors[0].dtype)
         tab = self.plan.ptr_table(tensors, what, elem_bytes=tensors[0].element_size(), stream=stream)
         return tab.data_ptr(), code
 
@@ -997,7 +983,7 @@ def fs_pack_mx4(mp: Mx4Plan, params: Sequence[torch.Tensor], out: torch.Tensor, 
     index = out.get_device()
     tab, code = mp._params(params, "params", index, stream)
     _launch(index, stream, lib().fs_pack_mx4, mp._h, tab, code, ptr, int(rank),
-            _scalar_ptr(seed, torch.int64, index, "seed"))
+            None if seed is None else _scalar_ptr(seed, torch.int64, index, "seed"))
 
 
 def fs_unpack_mx4(mp: Mx4Plan, gathered: torch.Tensor, params: Sequence[torch.Tensor], *, stream=None):

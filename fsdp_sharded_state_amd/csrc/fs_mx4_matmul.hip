@@ -558,26 +558,10 @@ bool big_offsets(const Mx4Mat &k, int64_t nb) {
            (jumps == 0 || k.chunk_stride < kBigMaxOffset / 4 / jumps);
 }
 
-int check_sizes(const char *what, int64_t m, int64_t n, int64_t k) {
-    if (m < 0 || n < 0 || k < 0) return fail(FS_E_INVAL, "%s: negative size", what);
-    if (m > INT32_MAX || n > INT32_MAX || k > INT32_MAX)
-        return fail(FS_E_OVERFLOW, "%s: more than 2^31 - 1 rows or columns", what);
-    return FS_OK;
-}
-
 }  // namespace
 
-extern "C" int fs_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t *bytes) {
-    clear_error();
-    const char *what = "fs_mx4_matmul_workspace";
-    if (!bytes) return fail(FS_E_INVAL, "%s: bytes is NULL", what);
-    if (int rc = check_sizes(what, m, n, k)) return rc;
-    *bytes = 0;
-    return FS_OK;
-}
-
 extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b, void *out, fs_dtype dtype, int64_t ldo,
-                             void *workspace, size_t bytes, hipStream_t stream) {
+                             hipStream_t stream) {
     clear_error();
     const char *what = "fs_mx4_matmul";
     if (!a || !b) return fail(FS_E_INVAL, "%s: a matrix is NULL", what);
@@ -589,8 +573,6 @@ extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b,
     if (a->cols != b->cols)
         return fail(FS_E_INVAL, "%s: a has %lld columns, b %lld", what, (long long)a->cols, (long long)b->cols);
     const int64_t m = a->rows, n = b->rows, k = a->cols, w = dtype == FS_BF16 ? 2 : 4;
-    int64_t need = 0;
-    if (int rc = fs_mx4_matmul_workspace(m, n, k, &need)) return rc;
     if (m == 0 || n == 0) return FS_OK;
     if (!out) return fail(FS_E_INVAL, "%s: out is NULL", what);
     if (misaligned(out, w)) return fail(FS_E_ALIGN, "%s: out not aligned to its element size", what);
@@ -600,16 +582,6 @@ extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b,
     struct { const void *p; int64_t bytes; } in[] = {{ka.codes, ac}, {ka.scales, as}, {kb.codes, bc}, {kb.scales, bs}};
     for (const auto &s : in)
         if (ranges_overlap(out, span, s.p, s.bytes)) return fail(FS_E_INVAL, "%s: out overlaps a matrix", what);
-    if (need > 0) {
-        if (!workspace) return fail(FS_E_INVAL, "%s: workspace is NULL", what);
-        if (misaligned(workspace, 16)) return fail(FS_E_ALIGN, "%s: workspace not 16-byte aligned", what);
-        if ((int64_t)bytes < need)
-            return fail(FS_E_INVAL, "%s: workspace too small (%zu < %lld bytes)", what, bytes, (long long)need);
-        if (ranges_overlap(workspace, need, out, span)) return fail(FS_E_INVAL, "%s: workspace overlaps out", what);
-        for (const auto &s : in)
-            if (ranges_overlap(workspace, need, s.p, s.bytes))
-                return fail(FS_E_INVAL, "%s: workspace overlaps a matrix", what);
-    }
     const int64_t nb = mx4_blocks(k), ld = m > 1 ? ldo : 0;
     (void)hipGetLastError();
     // By the tiles that there are for 256 CUs, measured over m from 1 to 4096, n and k from 512 to 11008 (us, in a graph).

@@ -671,23 +671,15 @@ int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype dtype, int64
  *                   summed in fp32; a bf16 output is rounded once.  With cols
  *                   = 0 the output is zero.
  *   dtype           FS_BF16 or FS_FP32.
- *   workspace (device) fs_mx4_matmul_workspace bytes, 16-byte aligned; may hold
- *                   anything, and is in use until the call's work is done, so
- *                   calls that may overlap in time need one each.
  * The order of the sums depends on the sizes alone, so results are
  * reproducible.  A linear layer y = x W^T and its gradients dx = dy W and
  * dW = dy^T x are three such products: of x and W by row, of dy by row and W
  * by column, of dy and x by column.
- * Errors: FS_E_INVAL (NULL pointers, different cols, strides too small, a
- * workspace too small or overlapping), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW,
- * FS_E_HIP.
+ * Errors: FS_E_INVAL (NULL pointers, different cols, strides too small, out
+ * overlapping a matrix), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW, FS_E_HIP.
  */
 int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b, void *out, fs_dtype dtype,
-                  int64_t ldo, void *workspace, size_t bytes, hipStream_t stream);
-
-/* fs_mx4_matmul_workspace -- workspace bytes (may be 0) of an m by n product
- * over k elements. */
-int fs_mx4_matmul_workspace(int64_t m, int64_t n, int64_t k, int64_t *bytes);
+                  int64_t ldo, hipStream_t stream);
 
 typedef struct fs_mx4_plan_s *fs_mx4_plan_t; /* opaque; host memory owned by the library */
 

@@ -1,5 +1,5 @@
 """Microscaled 4-bit shards without a GPU: the layout of the quantised shards
-against its definition, parameters as matrices, workspace sizes, and the
+against its definition, parameters as matrices, and the
 refusals of every call (each is refused before anything is launched)."""
 import ctypes
 import random
@@ -132,7 +132,7 @@ def test_calls_on_a_plan_without_tables_are_refused():
         assert call() == fs.FS_E_INVAL
 
 
-X, C, S, T, U, SEED, WS = (1 << 20, 1 << 30, (1 << 30) + (1 << 29), 1 << 31, (1 << 31) + (1 << 29), 1 << 12, 1 << 33)
+X, C, S, T, U, SEED = 1 << 20, 1 << 30, (1 << 30) + (1 << 29), 1 << 31, (1 << 31) + (1 << 29), 1 << 12
 
 
 def _mat(codes=C, scales=S, rows=40, cols=70, cs=48, ss=3, chunk=0, stride=0):
@@ -192,10 +192,10 @@ def test_dequantize_refusals(kw, code):
     assert _dequantize(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_mx4_dequantize")
 
 
-def _matmul(a="ok", b="ok", out=X, dtype=1, ldo=50, ws=WS, nbytes=1 << 40):
+def _matmul(a="ok", b="ok", out=X, dtype=1, ldo=50):
     a = _mat() if a == "ok" else a
     b = _mat(codes=T, scales=U, rows=50) if b == "ok" else b
-    return fs.lib().fs_mx4_matmul(a, b, out, dtype, ldo, ws, nbytes, None)
+    return fs.lib().fs_mx4_matmul(a, b, out, dtype, ldo, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -207,16 +207,6 @@ def _matmul(a="ok", b="ok", out=X, dtype=1, ldo=50, ws=WS, nbytes=1 << 40):
 ])
 def test_matmul_refusals(kw, code):
     assert _matmul(**kw) == code and fs.lib().fs_last_error().startswith(b"fs_mx4_matmul")
-
-
-def test_matmul_workspace_refusals():
-    L, n = fs.lib(), ctypes.c_int64()
-    assert L.fs_mx4_matmul_workspace(1, 1, 1, None) == fs.FS_E_INVAL
-    for m, k in ((-1, 1), (1, -1)):
-        assert L.fs_mx4_matmul_workspace(m, 5, k, ctypes.byref(n)) == fs.FS_E_INVAL
-    assert L.fs_mx4_matmul_workspace(1 << 31, 5, 5, ctypes.byref(n)) == fs.FS_E_OVERFLOW
-    for m, nn, k in ((0, 5, 5), (5, 0, 5), (5, 5, 0), (1, 1, 1), (8192, 8192, 8192), (64, 64, 1 << 20)):
-        assert L.fs_mx4_matmul_workspace(m, nn, k, ctypes.byref(n)) == 0 and n.value >= 0
 
 
 def test_binding_refusals():
