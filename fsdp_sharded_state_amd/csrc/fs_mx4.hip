@@ -180,16 +180,23 @@ struct Mx4Out {
     int64_t code_stride, scale_stride;
 };
 
+// Neighbours share the cache lines of codes and scales: a run of tiles to each XCD.
+__device__ __forceinline__ uint32_t tile_run(uint32_t id, uint32_t tiles) {
+    const uint32_t each = tiles / kXcds, rest = tiles % kXcds, xcd = id % kXcds;
+    return xcd * each + min(xcd, rest) + id / kXcds;
+}
+
 // Along rows alone, and back: a workgroup takes 16 rows by 128 elements, a lane 8 of them.
-constexpr int kRowTileCols = 128, kRowTileRows = kThreads * 8 / kRowTileCols;
+constexpr int kRowLanes = 16, kRowTileCols = 8 * kRowLanes, kRowTileRows = kThreads / kRowLanes;
 
 template <class T, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
                                                                      int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
                                                                      const uint64_t *__restrict__ seed_at) {
-    const int lq = threadIdx.x % (kRowTileCols / 8);
-    const int64_t r = (int64_t)(blockIdx.x / tiles_x) * kRowTileRows + threadIdx.x / (kRowTileCols / 8);
-    const int64_t c = (int64_t)(blockIdx.x % tiles_x) * kRowTileCols + 8 * lq, b = c / kMx4Block;
+    const uint32_t id = tile_run(blockIdx.x, gridDim.x);
+    const int lq = threadIdx.x % kRowLanes;
+    const int64_t r = (int64_t)(id / tiles_x) * kRowTileRows + threadIdx.x / kRowLanes;
+    const int64_t c = (int64_t)(id % tiles_x) * kRowTileCols + 8 * lq, b = c / kMx4Block;
     const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
     if (r >= rows || b >= nb) return;   // whole quads
     Raw8<T> v;
@@ -204,15 +211,16 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t row
 template <class T>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
                                                                   int64_t ldo, uint32_t tiles_x) {
-    const int64_t r = (int64_t)(blockIdx.x / tiles_x) * kRowTileRows + threadIdx.x / (kRowTileCols / 8);
-    const int64_t c = (int64_t)(blockIdx.x % tiles_x) * kRowTileCols + 8 * (threadIdx.x % (kRowTileCols / 8));
+    const uint32_t id = tile_run(blockIdx.x, gridDim.x);
+    const int64_t r = (int64_t)(id / tiles_x) * kRowTileRows + threadIdx.x / kRowLanes;
+    const int64_t c = (int64_t)(id % tiles_x) * kRowTileCols + 8 * (threadIdx.x % kRowLanes);
     if (r >= rows || c >= cols) return;
     int64_t code, scale;
     m.row((uint32_t)r, &code, &scale);
     const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
-    with_past(sizeof(T) == 2 && on16(out) && ldo * sizeof(T) % 16 == 0, [&](auto past) {
-        store8<past>(out + r * ldo + c, w, scale_value(m.scales[scale + c / kMx4Block]), (int)imin(8, cols - c));
-    });
+    const float f = scale_value(m.scales[scale + c / kMx4Block]);
+    with_past(sizeof(T) == 2 && on16(out) && ldo * sizeof(T) % 16 == 0,
+              [&](auto past) { store8<past>(out + r * ldo + c, w, f, (int)imin(8, cols - c)); });
 }
 
 // Along columns, with or without rows: a workgroup takes 128 by 128 elements.
@@ -246,9 +254,7 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
                                                                      Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
     constexpr int kPitch = kColTile * sizeof(T) + 16;   // bytes: the writes of 16 bytes by 16 lanes a row go on evenly over the banks
     __shared__ __attribute__((aligned(16))) uint8_t lds[kColTile * kPitch];
-    // neighbours share the cache lines of codes that they write: a run of tiles to each XCD
-    const uint32_t each = gridDim.x / kXcds, rest = gridDim.x % kXcds, xcd = blockIdx.x % kXcds;
-    const uint32_t id = xcd * each + min(xcd, rest) + blockIdx.x / kXcds;
+    const uint32_t id = tile_run(blockIdx.x, gridDim.x);
     const int64_t r0 = (int64_t)(id / tiles_x) * kColTile, c0 = (int64_t)(id % tiles_x) * kColTile;
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
@@ -267,16 +273,23 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
         __builtin_memcpy(__builtin_assume_aligned(lds + lr * kPitch + lq * sizeof v[i], 16), &v[i], sizeof v[i]);
     }
     if (ROWS) {
+        constexpr int kStep = kThreads / kColLanes;   // rows between a lane's loads
+        const int lq = threadIdx.x % kColLanes;
+        const int64_t r1 = r0 + threadIdx.x / kColLanes, b = c0 / kMx4Block + lq / 4;
+        uint8_t *codes = by_row.codes + r1 * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3);
+        uint8_t *scales = by_row.scales + r1 * by_row.scale_stride + b;
+        uint64_t group = 4 * (uint64_t)(r1 * nbr + b) + (lq & 3);
 #pragma unroll
         for (int i = 0; i < kColSteps; ++i) {
-            const int q = i * kThreads + threadIdx.x, lq = q % kColLanes;
-            const int64_t r = r0 + q / kColLanes, b = c0 / kMx4Block + lq / 4;
             uint32_t s;
-            const uint32_t code = encode8<STOCHASTIC>(v[i], seed, 4 * (uint64_t)(r * nbr + b) + (lq & 3), 0, &s);
-            if (r < rows && b < nbr) {
-                *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
-                if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
+            const uint32_t code = encode8<STOCHASTIC>(v[i], seed, group, 0, &s);
+            if (r1 + i * kStep < rows && b < nbr) {
+                *reinterpret_cast<uint32_t *>(codes) = code;
+                if ((lq & 3) == 0) *scales = (uint8_t)s;
             }
+            codes += kStep * by_row.code_stride;
+            scales += kStep * by_row.scale_stride;
+            group += 4 * kStep * (uint64_t)nbr;
         }
     }
     __syncthreads();
@@ -495,12 +508,14 @@ int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, M
     const int64_t run = m->chunk_rows ? imin(m->chunk_rows, m->rows) : m->rows;   // rows of a chunk
     if ((run > 1 && (m->code_stride < nb * kMx4BlockBytes || m->scale_stride < nb)))
         return fail(FS_E_INVAL, "%s: the rows of %s overlap", what, name);
-    if (misaligned(m->codes, 16) || (m->code_stride & 15) || (m->chunk_rows && (m->chunk_stride & 15)))
-        return fail(FS_E_ALIGN, "%s: the codes of %s are not on 16 bytes", what, name);
     const int64_t chunks = m->chunk_rows ? (m->rows + m->chunk_rows - 1) / m->chunk_rows : 1;
-    if (m->code_stride > kMost / run || m->scale_stride > kMost / run || (chunks > 1 && m->chunk_stride > kMost / chunks))
+    if (misaligned(m->codes, 16) || (run > 1 && (m->code_stride & 15)) || (chunks > 1 && (m->chunk_stride & 15)))
+        return fail(FS_E_ALIGN, "%s: the codes of %s are not on 16 bytes", what, name);
+    if ((run > 1 && (m->code_stride > kMost / run || m->scale_stride > kMost / run)) ||
+        (chunks > 1 && m->chunk_stride > kMost / chunks))
         return fail(FS_E_OVERFLOW, "%s: the strides of %s are too large", what, name);
-    const int64_t codes = (run - 1) * m->code_stride + nb * kMx4BlockBytes, scales = (run - 1) * m->scale_stride + nb;
+    const int64_t codes = (run > 1 ? (run - 1) * m->code_stride : 0) + nb * kMx4BlockBytes;
+    const int64_t scales = (run > 1 ? (run - 1) * m->scale_stride : 0) + nb;
     // the chunks' codes (or scales) follow each other; the two may lie between each other, as in a gathered buffer
     if (chunks > 1 && (m->chunk_stride < codes || m->chunk_stride < scales))
         return fail(FS_E_INVAL, "%s: the chunks of %s overlap", what, name);
