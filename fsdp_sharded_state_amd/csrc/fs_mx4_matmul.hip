@@ -458,7 +458,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWaves * S::kPerCu / 4) void matmul
     };
     constexpr int kBehind = 2 * kLoads;   // loads of the two latest steps
 
-    const int32_t groups = (nb + 15) / 16;   // of four steps
+    // Groups of four steps.  Without a block there is one all the same, which multiplies zeros: the way to the next tile
+    // leads through it.
+    const int32_t groups = nb > 0 ? (nb + 15) / 16 : 1;
     uint32_t tile = blockIdx.x, tm, tn;
     tile_of(tile, tiles_m, tiles_n, &tm, &tn);
     aim((int64_t)tm * BM, (int64_t)tn * BN);

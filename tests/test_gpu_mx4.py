@@ -419,6 +419,16 @@ def test_matmul_of_nothing():
     fs.fs_mx4_matmul(fs.fs_mx4_empty(5, 64), fs.fs_mx4_empty(0, 64), torch.empty(5, 0, device="cuda"))
 
 
+@pytest.mark.parametrize("m,n", [(300, 700), (1100, 1300), (2100, 2300), (5000, 4700)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_matmul_without_columns_at_every_size(m, n, dtype):
+    """No term at all: zeros, also where a workgroup takes one tile after the other."""
+    say(f"no columns {m} {n} {dtype}")
+    out = torch.full((m, n + 3), 3.0, dtype=DT[dtype], device="cuda")
+    fs.fs_mx4_matmul(fs.fs_mx4_empty(m, 0), fs.fs_mx4_empty(n, 0), out[:, :n])
+    assert (out[:, :n] == 0).all() and (out[:, n:] == 3).all()
+
+
 @pytest.mark.parametrize("m,n,k", [(2048, 4096, 4096), (1000, 5000, 2304), (4096, 512, 8192), (7, 11008, 4096), (64, 4096, 11008)])
 def test_matmul_large_exact_sums(m, n, k):
     """Small integers at one scale: every partial sum is an integer (in units
