@@ -925,6 +925,7 @@ class Mx4Plan:
         self.shard_blocks, self.shard_bytes = info.shard_blocks, info.shard_bytes
         self.gathered_bytes, self.workspace_bytes = info.gathered_bytes, info.workspace_bytes
         self.workspace: Optional[torch.Tensor] = None
+        self._earlier: list = []    # workspaces of earlier uploads, which launches and captured graphs may still read
 
     def close(self):
         h = self.__dict__.pop("_h", None)
@@ -937,6 +938,8 @@ class Mx4Plan:
     def upload(self, device="cuda", stream=None) -> "Mx4Plan":
         ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=device)
         _launch(ws.get_device(), stream, lib().fs_mx4_plan_upload, self._h, ws.data_ptr(), ws.numel())
+        if self.workspace is not None:
+            self._earlier.append(self.workspace)
         self.workspace = ws
         return self
 

@@ -12,6 +12,7 @@ namespace {
 constexpr int kQuads = kThreads / 4;                       // blocks a workgroup handles at a time
 constexpr int kTileSteps = kMx4TileBlocks / kQuads;        // a lane's quarters of a tile
 static_assert(kTileSteps * kQuads == kMx4TileBlocks, "a tile is whole steps");
+static_assert(kThreads >= kMx4TileBlocks, "a thread for every block of a tile or pad");
 
 // ------------------------------------------------------------------ shards --
 

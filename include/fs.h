@@ -671,8 +671,9 @@ int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype dtype, int64
  *                   summed in fp32; a bf16 output is rounded once.  With cols
  *                   = 0 the output is zero.
  *   dtype           FS_BF16 or FS_FP32.
- * The order of the sums depends on the sizes alone, so results are
- * reproducible.  A linear layer y = x W^T and its gradients dx = dy W and
+ * Elements that fill up a row's last block take part like the others: +0, as
+ * fs_mx4_quantize leaves them.  The order of the sums depends on the sizes and
+ * strides alone, so results are reproducible.  A linear layer y = x W^T and its gradients dx = dy W and
  * dW = dy^T x are three such products: of x and W by row, of dy by row and W
  * by column, of dy and x by column.
  * Errors: FS_E_INVAL (NULL pointers, different cols, strides too small, out
@@ -707,7 +708,8 @@ int fs_mx4_plan(fs_plan_t plan, fs_mx4_plan_t *out);
 int fs_mx4_plan_info(fs_mx4_plan_t p, fs_mx4_plan_info_t *out);
 /* First block of parameter i's run in rank r's shard, and its element count (0: none). */
 int fs_mx4_plan_piece(fs_mx4_plan_t p, int32_t i, int32_t rank, int64_t *first_block, int64_t *numel);
-/* As fs_plan_upload. */
+/* As fs_plan_upload.  A later upload takes another workspace; what was launched
+ * or captured before it goes on reading the earlier one. */
 int fs_mx4_plan_upload(fs_mx4_plan_t p, void *workspace, size_t bytes, hipStream_t stream);
 void fs_mx4_plan_destroy(fs_mx4_plan_t p);
 

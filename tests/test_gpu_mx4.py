@@ -654,6 +654,70 @@ def test_captured_step_replays_with_new_values():
     assert not torch.equal(seen[0], seen[1])
 
 
+def test_two_captured_graphs_at_once():
+    """Two graphs of the same calls on the same plan, each into buffers of its own, replayed side by side on
+    two streams; a second upload comes between their captures."""
+    shapes, world, acc, plan, _ = _step_buffers()
+    mp = fs.fs_mx4_plan(plan).upload()
+    params = [_values(s, "bf16", i) for i, s in enumerate(shapes)]
+    quantised = _random_matrix(300, 2048, 1), _random_matrix(200, 2048, 2)
+    a, b = (fs.Mx4Matrix(*q, 2048) for q in quantised)
+    sets = [(torch.empty(mp.gathered_bytes, dtype=torch.uint8, device="cuda"), torch.empty(plan.shard_numel, device="cuda"),
+             torch.empty(300, 200, device="cuda"), fs.fs_mx4_empty(300, 200), fs.fs_mx4_empty(200, 300), _seed(k))
+            for k in range(2)]
+
+    def step(gathered, g32, out, row, col, seed):
+        fs.fs_pack_mx4(mp, params, gathered, seed=seed)
+        fs.fs_reduce_shard_mx4(mp, [gathered[:mp.shard_bytes]] * (world * acc), g32, rank=0, grad_acc=acc)
+        fs.fs_mx4_matmul(a, b, out)
+        fs.fs_mx4_quantize(out, row, col, seed=seed)
+
+    def state(s):
+        return [t.clone() for t in (s[0], s[1], s[2], s[3].codes, s[3].scales, s[4].codes, s[4].scales)]
+
+    want = []
+    for s in sets:
+        step(*s)
+        want.append(state(s))
+    torch.cuda.synchronize()
+    graphs, streams = [torch.cuda.CUDAGraph() for _ in sets], [torch.cuda.Stream() for _ in sets]
+    for g, s in zip(graphs, sets):
+        with torch.cuda.graph(g):
+            step(*s)
+        mp.upload()
+    for turn in range(4):
+        for s in sets:
+            for t in (s[0], s[1], s[2], s[3].codes, s[4].codes):
+                t.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, st in zip(graphs, streams):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for k, s in enumerate(sets):
+            assert all(torch.equal(p, q) for p, q in zip(state(s), want[k])), f"turn {turn}, graph {k}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [33, 4096])
+def test_one_row_has_no_stride(dtype, cols):
+    """The strides of matrices of one row are not looked at: here ones that no larger matrix could have."""
+    nb = ref.blocks(cols)
+    x = _values((1, cols), dtype, 3)
+    codes = torch.empty(16 * nb, dtype=torch.uint8, device="cuda").as_strided((1, 16 * nb), (5, 1))
+    scales = torch.empty(nb, dtype=torch.uint8, device="cuda").as_strided((1, nb), (0, 1))
+    q, out = fs.Mx4Matrix(codes, scales, cols), torch.empty(cols, device="cuda").as_strided((1, cols), (1, 1))
+    fs.fs_mx4_quantize(x.as_strided((1, cols), (7, 1)), q)
+    c, s = ref.encode_matrix(_f64(x))
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    fs.fs_mx4_dequantize(q, out)
+    assert np.array_equal(_f64(out), _decoded(codes, scales, cols))
+    y = torch.empty(1, dtype=torch.float32, device="cuda").as_strided((1, 1), (0, 1))
+    fs.fs_mx4_matmul(q, q, y)
+    _check_product((codes, scales), (codes, scales), y, 1, 1, cols)
+
+
 def test_other_streams_and_threads():
     """Each thread on its own stream, each with its own buffers, gives the single-threaded results."""
     shapes, world, acc, plan, _ = _step_buffers()
