@@ -228,7 +228,9 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
 // Its rows' blocks come straight from the loads, as above.  Its columns' come from a copy in
 // LDS, where a lane takes 32 rows of two columns (of one in fp32), two blocks of its own: reads
 // of whole rows by the wave, and no joins between lanes.
-constexpr int kColTile = 128, kColLanes = kColTile / 8, kColSteps = kColTile * kColLanes / kThreads;
+constexpr int kColTileRows = 128;
+template <class T>
+constexpr int kColTileCols = 256 / sizeof(T);
 
 // The blocks in column `at` of a wave's 32 rows of LDS words: one for fp32, two for bf16.
 __device__ __forceinline__ void column_raws(Raw8<float> (&v)[1][4], const uint32_t *w) {
@@ -253,10 +255,15 @@ template <class T, bool ROWS, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
                                                                      int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
                                                                      Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
-    constexpr int kPitch = kColTile * sizeof(T) + 16;   // bytes: the writes of 16 bytes by 16 lanes a row go on evenly over the banks
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kColTile * kPitch];
+    constexpr int kCols = kColTileCols<T>, kColLanes = kCols / 8, kColSteps = kColTileRows * kColLanes / kThreads;
+    constexpr int kColBlocks = kColTileRows / kMx4Block;   // of a column
+    // Bytes of a row in LDS, and more between blocks of them: neither the writes of rows nor the reads of four blocks'
+    // words by the lanes of a quad meet in a bank.
+    constexpr int kPitch = 256 + 16, kBetween = 64;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kColTileRows * kPitch + kColBlocks * kBetween];
+    auto lds_row = [&](int r) { return lds + r * kPitch + r / kMx4Block * kBetween; };
     const uint32_t id = tile_run(blockIdx.x, gridDim.x);
-    const int64_t r0 = (int64_t)(id / tiles_x) * kColTile, c0 = (int64_t)(id % tiles_x) * kColTile;
+    const int64_t r0 = (int64_t)(id / tiles_x) * kColTileRows, c0 = (int64_t)(id % tiles_x) * kCols;
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
     Raw8<T> v[kColSteps];
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
 #pragma unroll
     for (int i = 0; i < kColSteps; ++i) {
         const int q = i * kThreads + threadIdx.x, lr = q / kColLanes, lq = q % kColLanes;
-        __builtin_memcpy(__builtin_assume_aligned(lds + lr * kPitch + lq * sizeof v[i], 16), &v[i], sizeof v[i]);
+        __builtin_memcpy(__builtin_assume_aligned(lds_row(lr) + lq * sizeof v[i], 16), &v[i], sizeof v[i]);
     }
     if (ROWS) {
         constexpr int kStep = kThreads / kColLanes;   // rows between a lane's loads
@@ -294,29 +301,26 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
         }
     }
     __syncthreads();
-    constexpr int kWide = 4 / sizeof(T), kWords = kColTile / kWide;   // columns a lane, lanes a row
-    constexpr int kItems = kWords * (kColTile / kMx4Block) / kThreads;
+    constexpr int kWide = 4 / sizeof(T);   // columns a lane
+    static_assert(kCols / kWide * kColBlocks == kThreads, "a lane takes the blocks of one word's columns");
+    const int lb = threadIdx.x % kColBlocks, lc = threadIdx.x / kColBlocks;   // a quad's codes follow each other
+    const int64_t b = r0 / kMx4Block + lb;
+    if (b >= nbc) return;
+    uint32_t w[kMx4Block];
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int q = i * kThreads + threadIdx.x, lb = q / kWords, lc = q % kWords;
-        const int64_t b = r0 / kMx4Block + lb;
-        if (b >= nbc) continue;
-        uint32_t w[kMx4Block];
+    for (int k = 0; k < kMx4Block; ++k) w[k] = *reinterpret_cast<const uint32_t *>(lds_row(lb * kMx4Block) + k * kPitch + lc * 4);
+    Raw8<T> e[kWide][4];
+    column_raws(e, w);
 #pragma unroll
-        for (int k = 0; k < kMx4Block; ++k) w[k] = *reinterpret_cast<const uint32_t *>(lds + (lb * kMx4Block + k) * kPitch + lc * 4);
-        Raw8<T> e[kWide][4];
-        column_raws(e, w);
+    for (int j = 0; j < kWide; ++j) {
+        const int64_t c = c0 + lc * kWide + j;
+        const uint32_t s = scale_byte<STOCHASTIC>(max(max(amax8(e[j][0]), amax8(e[j][1])), max(amax8(e[j][2]), amax8(e[j][3]))));
+        uint32_t code[4];
 #pragma unroll
-        for (int j = 0; j < kWide; ++j) {
-            const int64_t c = c0 + lc * kWide + j;
-            const uint32_t s = scale_byte<STOCHASTIC>(max(max(amax8(e[j][0]), amax8(e[j][1])), max(amax8(e[j][2]), amax8(e[j][3]))));
-            uint32_t code[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) code[k] = encode8_at<STOCHASTIC>(e[j][k], s, seed, 4 * (uint64_t)(c * nbc + b) + k, 1);
-            if (c < cols) {
-                *reinterpret_cast<u32x4 *>(by_col.codes + c * by_col.code_stride + b * kMx4BlockBytes) = u32x4{code[0], code[1], code[2], code[3]};
-                by_col.scales[c * by_col.scale_stride + b] = (uint8_t)s;
-            }
+        for (int k = 0; k < 4; ++k) code[k] = encode8_at<STOCHASTIC>(e[j][k], s, seed, 4 * (uint64_t)(c * nbc + b) + k, 1);
+        if (c < cols) {
+            *reinterpret_cast<u32x4 *>(by_col.codes + c * by_col.code_stride + b * kMx4BlockBytes) = u32x4{code[0], code[1], code[2], code[3]};
+            by_col.scales[c * by_col.scale_stride + b] = (uint8_t)s;
         }
     }
 }
@@ -613,7 +617,7 @@ extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dty
     if (by_col)
         if (int rc = check_out(what, "by_col", by_col, cols, rows, &col, spans, &count)) return rc;
     uint32_t across, tiles;
-    if (int rc = by_col ? mat_tiles(what, rows, cols, kColTile, kColTile, &across, &tiles)
+    if (int rc = by_col ? mat_tiles(what, rows, cols, kColTileRows, dtype == FS_BF16 ? kColTileCols<uint16_t> : kColTileCols<float>, &across, &tiles)
                         : mat_tiles(what, rows, cols, kRowTileRows, kRowTileCols, &across, &tiles))
         return rc;
     if (tiles == 0) return FS_OK;
