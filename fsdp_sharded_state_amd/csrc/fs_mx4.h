@@ -39,8 +39,8 @@ __device__ __forceinline__ u32x4 ld16_any(const void *p) { return *(const Global
 __device__ __forceinline__ void st16_any(void *p, u32x4 v) { *(Global<u32x4_any> *)reinterpret_cast<uintptr_t>(p) = v; }
 // Past the caches, on 16 bytes.  Elements pass through once, and what a call
 // leaves in the caches to be written back costs the next one: copy-in and copy-out of one 7B block
-// in bf16 take 206 us without, 156 with.  Off 16 bytes lanes share sectors, which the caches have to join, and so it is
-// with the two pieces of 8 fp32 values (copy-out of 45M: 34 us through the caches, 84 past them).
+// in bf16 take 206 us without, 156 with.  Off 16 bytes lanes share sectors, which the caches have to join
+// (45M fp32 elements to odd addresses: 34 us through the caches, 84 past them).
 // The two kinds of access are chosen by a template argument: the compiler makes one of a choice beside them.
 template <bool PAST>
 __device__ __forceinline__ u32x4 ld16_el(const void *p) {
@@ -73,36 +73,85 @@ struct Raw8<float> {
 
 __device__ __forceinline__ bool on16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// `valid` (any value) elements from p on, zeros after them.
+__device__ __forceinline__ uint32_t word(const u32x4 &v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+// Elements of 16 bytes, and units of that size in a lane's eight.
+template <class T>
+constexpr int kUnit = 16 / sizeof(T);
+template <class T>
+constexpr int kUnits = 8 / kUnit<T>;
+
+// `valid` (any value) elements of a unit at p, zeros after them.
 template <bool PAST>
-__device__ __forceinline__ void load8(Raw8<uint16_t> &r, const uint16_t *p, int valid) {
-    if (valid >= 8) {
-        r.v = ld16_el<PAST>(p);
-    } else {
-        uint32_t w[4];
+__device__ __forceinline__ u32x4 load_unit(const uint16_t *p, int valid) {
+    if (valid >= 8) return ld16_el<PAST>(p);
+    uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t lo = 2 * k < valid ? ld(p + 2 * k) : 0, hi = 2 * k + 1 < valid ? ld(p + 2 * k + 1) : 0;
-            w[k] = lo | (hi << 16);
-        }
-        r.v = u32x4{w[0], w[1], w[2], w[3]};
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = 2 * k < valid ? ld(p + 2 * k) : 0, hi = 2 * k + 1 < valid ? ld(p + 2 * k + 1) : 0;
+        w[k] = lo | (hi << 16);
+    }
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+template <bool PAST>
+__device__ __forceinline__ u32x4 load_unit(const float *p, int valid) {
+    if (valid >= 4) return ld16_el<PAST>(p);
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = k < valid ? __float_as_uint(ld(p + k)) : 0u;
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+template <bool PAST>
+__device__ __forceinline__ void store_unit(uint16_t *p, const u32x4 &v, int valid) {
+    if (valid >= 8) {
+        st16_el<PAST>(p, v);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k < valid) st(p + k, (uint16_t)(word(v, k >> 1) >> (16 * (k & 1))));
     }
 }
 template <bool PAST>
-__device__ __forceinline__ void load8(Raw8<float> &r, const float *p, int valid) {
-    if (valid >= 8) {
-        r.v[0] = ld16_el<PAST>(p);
-        r.v[1] = ld16_el<PAST>(p + 4);
+__device__ __forceinline__ void store_unit(float *p, const u32x4 &v, int valid) {
+    if (valid >= 4) {
+        st16_el<PAST>(p, v);
     } else {
-        uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) w[k] = k < valid ? __float_as_uint(ld(p + k)) : 0u;
-        r.v[0] = u32x4{w[0], w[1], w[2], w[3]};
-        r.v[1] = u32x4{w[4], w[5], w[6], w[7]};
+        for (int k = 0; k < 4; ++k)
+            if (k < valid) st(p + k, __uint_as_float(word(v, k)));
     }
 }
 
-__device__ __forceinline__ uint32_t word(const u32x4 &v, int k) { return k == 0 ? v.x : k == 1 ? v.y : k == 2 ? v.z : v.w; }
+// The lanes of a wave meet, their LDS accesses before this place before those
+// after it.  (The hardware keeps a wave's LDS accesses in order; this keeps the compiler to it.)
+__device__ __forceinline__ void wave_meets() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
+// A lane's eight fp32 values are two units.  With each lane at its own two, an access of the wave would hold half of
+// each cache line.  So units go to the lanes in turn, lane l taking
+// units l and 64 + l of the wave's 128, and are exchanged through 2 KB of LDS for 2l and 2l + 1, its own: one 7B block
+// in fp32 both ways 397 us -> 308, its shard's reduce 39.3 -> 34.9, 8192 by 11008 from fp32 92 -> 78 and back 99 -> 62.
+__device__ __forceinline__ Raw8<uint16_t> own_units(const u32x4 (&v)[1], u32x4 *) { return Raw8<uint16_t>{v[0]}; }
+__device__ __forceinline__ Raw8<float> own_units(const u32x4 (&v)[2], u32x4 *of_wave) {
+    const int lane = threadIdx.x & 63;
+    of_wave[lane] = v[0];
+    of_wave[64 + lane] = v[1];
+    wave_meets();
+    const Raw8<float> r{{of_wave[2 * lane], of_wave[2 * lane + 1]}};
+    wave_meets();
+    return r;
+}
+// And back.
+__device__ __forceinline__ void units_in_turn(u32x4 (&v)[2], const float (&own)[8], u32x4 *of_wave) {
+    const int lane = threadIdx.x & 63;
+    __builtin_memcpy(&of_wave[2 * lane], own, 32);
+    wave_meets();
+    v[0] = of_wave[lane];
+    v[1] = of_wave[64 + lane];
+    wave_meets();
+}
 
 // Element k as fp32.
 __device__ __forceinline__ float elem(const Raw8<uint16_t> &r, int k) {
@@ -278,36 +327,17 @@ __device__ __forceinline__ u32x4 decode8_bf16(uint32_t c, float scale) {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, scale, 3))};
 }
 
-// The first `valid` of the 8 values of codes c to p.
-template <bool PAST>
-__device__ __forceinline__ void store8(uint16_t *p, uint32_t c, float scale, int valid) {
-    const u32x4 v = decode8_bf16(c, scale);
-    if (valid >= 8) {
-        st16_el<PAST>(p, v);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < valid) st(p + k, (uint16_t)(word(v, k >> 1) >> (16 * (k & 1))));
-    }
+// The values of a unit's codes, the low bits of c.
+__device__ __forceinline__ u32x4 decode_unit(uint16_t, uint32_t c, float scale) { return decode8_bf16(c, scale); }
+__device__ __forceinline__ u32x4 decode_unit(float, uint32_t c, float scale) {
+    const f32x2 v[2] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1)};
+    return __builtin_bit_cast(u32x4, v);
 }
-template <bool PAST>
-__device__ __forceinline__ void store8(float *p, const float *v, int valid) {
-    if (valid >= 8) {
-        u32x4 w[2];
-        __builtin_memcpy(w, v, sizeof w);
-        st16_el<PAST>(p, w[0]);
-        st16_el<PAST>(p + 4, w[1]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (k < valid) st(p + k, v[k]);
-    }
-}
-template <bool PAST>
-__device__ __forceinline__ void store8(float *p, uint32_t c, float scale, int valid) {
-    float v[8];
-    decode8(v, c, scale);
-    store8<PAST>(p, v, valid);
+// Those codes, of unit `unit` from p on.
+template <class T>
+__device__ __forceinline__ uint32_t unit_codes(const uint8_t *p, int64_t unit) {
+    if (sizeof(T) == 2) return ld(reinterpret_cast<const uint32_t *>(p) + unit);
+    return ld(reinterpret_cast<const uint16_t *>(p) + unit);
 }
 
 // A matrix of blocks, by value.  Rows fit in 31 bits, so a row's chunk comes

@@ -14,6 +14,10 @@ constexpr int kTileSteps = kMx4TileBlocks / kQuads;        // a lane's quarters 
 static_assert(kTileSteps * kQuads == kMx4TileBlocks, "a tile is whole steps");
 static_assert(kThreads >= kMx4TileBlocks, "a thread for every block of a tile or pad");
 
+// The waves of a workgroup that exchange units through LDS: those of fp32 elements, the others need none.
+template <class T>
+constexpr int kWavesExchanging = kUnits<T> > 1 ? kThreads / 64 : 1;
+
 // ------------------------------------------------------------------ shards --
 
 // A tile's codes and scales go through LDS: 16 bytes a lane are stored for the
@@ -25,6 +29,7 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
                                                             uint8_t *__restrict__ out, int32_t first_rank,
                                                             int64_t shard_blocks, int64_t shard_bytes,
                                                             const uint64_t *__restrict__ seed_at) {
+    __shared__ u32x4 lds_units[kWavesExchanging<T>][128];
     __shared__ uint32_t lds_codes[kMx4TileBlocks * 4];
     __shared__ __attribute__((aligned(4))) uint8_t lds_scales[kMx4TileBlocks];
     const int tid = threadIdx.x;
@@ -44,19 +49,24 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
     const T *src = static_cast<const T *>(params[t.param]) + t.src;
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const uint64_t group = 4 * (uint64_t)(t.rank * shard_blocks + t.blk);
-    Raw8<T> r[kTileSteps];
+    constexpr int U = kUnits<T>, E = kUnit<T>;
+    const int first = (tid & ~63) * U + (tid & 63);
+    u32x4 v[kTileSteps][U];
     with_past(on16(src), [&](auto past) {
 #pragma unroll
-        for (int i = 0; i < kTileSteps; ++i) {
-            const int q = i * kThreads + tid;
-            load8<past>(r[i], src + 8 * q, t.n - 8 * q);
-        }
+        for (int i = 0; i < kTileSteps; ++i)
+#pragma unroll
+            for (int h = 0; h < U; ++h) {
+                const int at = E * (i * kThreads * U + first + 64 * h);
+                v[i][h] = load_unit<past>(src + at, t.n - at);
+            }
     });
 #pragma unroll
     for (int i = 0; i < kTileSteps; ++i) {
         const int q = i * kThreads + tid;
+        const Raw8<T> r = own_units(v[i], lds_units[U > 1 ? tid >> 6 : 0]);
         uint32_t s;
-        lds_codes[q] = encode8<STOCHASTIC>(r[i], seed, group + q, 0, &s);
+        lds_codes[q] = encode8<STOCHASTIC>(r, seed, group + q, 0, &s);
         if ((tid & 3) == 0) lds_scales[q >> 2] = (uint8_t)s;
     }
     __syncthreads();
@@ -77,22 +87,23 @@ __global__ __launch_bounds__(kThreads) void unpack_mx4_kernel(const Mx4Tile *__r
     const Mx4Tile t = tiles[blockIdx.x];
     T *dst = static_cast<T *>(params[t.param]) + t.src;
     const uint8_t *shard = gathered + t.rank * shard_bytes;
-    const uint32_t *codes = reinterpret_cast<const uint32_t *>(shard + t.blk * kMx4BlockBytes);
+    const uint8_t *codes = shard + t.blk * kMx4BlockBytes;
     const uint8_t *scales = shard + shard_blocks * kMx4BlockBytes + t.blk;
-    uint32_t c[kTileSteps], s[kTileSteps];
+    constexpr int E = kUnit<T>, kSteps = kMx4Tile / E / kThreads;
+    uint32_t c[kSteps], s[kSteps];
 #pragma unroll
-    for (int i = 0; i < kTileSteps; ++i) {
+    for (int i = 0; i < kSteps; ++i) {
         const int q = i * kThreads + tid;
-        if (8 * q < t.n) {
-            c[i] = codes[q];
-            s[i] = scales[q >> 2];
+        if (E * q < t.n) {
+            c[i] = unit_codes<T>(codes, q);
+            s[i] = ld(scales + q / (kMx4Block / E));
         }
     }
-    with_past(sizeof(T) == 2 && on16(dst), [&](auto past) {
+    with_past(on16(dst), [&](auto past) {
 #pragma unroll
-        for (int i = 0; i < kTileSteps; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             const int q = i * kThreads + tid;
-            if (8 * q < t.n) store8<past>(dst + 8 * q, c[i], scale_value(s[i]), t.n - 8 * q);
+            if (E * q < t.n) store_unit<past>(dst + E * q, decode_unit(T{}, c[i], scale_value(s[i])), t.n - E * q);
         }
     });
 }
@@ -142,6 +153,7 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
                                                               const Mx4Run *__restrict__ gaps, Mx4Slices slices,
                                                               int nterms, int first_pass, float divide, float scale,
                                                               float *__restrict__ out, int64_t shard_blocks) {
+    __shared__ u32x4 lds_units[kThreads / 64][128];
     const int tid = threadIdx.x;
     const uint32_t id = blockIdx.x;
     if (id >= ntiles * kParts) {   // elements of no piece
@@ -153,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
     const Mx4Tile t = tiles[at.tile];
     if (at.part == 0 && tid < t.fill) out[t.elem + t.n + tid] = 0.f;
     const int q = at.part * kThreads + tid, valid = t.n - 8 * q;
-    if (valid <= 0) return;
+    if (t.n - 8 * (q & ~63) <= 0) return;   // whole waves
     const int64_t code0 = t.blk * kMx4BlockBytes, scale0 = shard_blocks * kMx4BlockBytes + t.blk;
     float *dst = out + t.elem + 8 * q;
     float acc[8];
@@ -162,16 +174,24 @@ __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__r
         acc[k] = -0.f;   // adds nothing to any value, zeros of either sign among them
         if (!first_pass && k < valid) acc[k] = dst[k];
     }
-    int j = 0;
-    for (; j + 8 <= nterms; j += 8) add_slices<8>(acc, slices, j, code0, scale0, q);
-    if (j + 4 <= nterms) {
-        add_slices<4>(acc, slices, j, code0, scale0, q);
-        j += 4;
+    if (valid > 0) {
+        int j = 0;
+        for (; j + 8 <= nterms; j += 8) add_slices<8>(acc, slices, j, code0, scale0, q);
+        if (j + 4 <= nterms) {
+            add_slices<4>(acc, slices, j, code0, scale0, q);
+            j += 4;
+        }
+        for (; j < nterms; ++j) add_slices<1>(acc, slices, j, code0, scale0, q);
     }
-    for (; j < nterms; ++j) add_slices<1>(acc, slices, j, code0, scale0, q);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] = divide != 0.f ? acc[k] / divide : acc[k] * scale;
-    with_past(on16(out + t.elem), [&](auto past) { store8<past>(dst, acc, valid); });
+    u32x4 v[2];
+    units_in_turn(v, acc, lds_units[tid >> 6]);
+    const int first = 8 * (q & ~63) + 4 * (tid & 63);
+    with_past(on16(out + t.elem), [&](auto past) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) store_unit<past>(out + t.elem + first + 256 * h, v[h], t.n - first - 256 * h);
+    });
 }
 
 // ---------------------------------------------------------------- matrices --
@@ -194,34 +214,56 @@ template <class T, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
                                                                      int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
                                                                      const uint64_t *__restrict__ seed_at) {
+    constexpr int U = kUnits<T>, E = kUnit<T>, kRowUnits = kRowTileCols / E;
+    __shared__ u32x4 lds_units[kWavesExchanging<T>][128];
     const uint32_t id = tile_run(blockIdx.x, gridDim.x);
-    const int lq = threadIdx.x % kRowLanes;
-    const int64_t r = (int64_t)(id / tiles_x) * kRowTileRows + threadIdx.x / kRowLanes;
-    const int64_t c = (int64_t)(id % tiles_x) * kRowTileCols + 8 * lq, b = c / kMx4Block;
-    const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
+    const int tid = threadIdx.x, lq = tid % kRowLanes;
+    const int64_t r0 = (int64_t)(id / tiles_x) * kRowTileRows, c0 = (int64_t)(id % tiles_x) * kRowTileCols;
+    u32x4 v[U];
+    with_past(on16(x) && ldx * sizeof(T) % 16 == 0, [&](auto past) {
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+            const int u = (tid & ~63) * U + 64 * h + (tid & 63);
+            const int64_t r = r0 + u / kRowUnits, c = c0 + E * (u % kRowUnits);
+            v[h] = load_unit<past>(x + r * ldx + c, r < rows ? (int)imax(0, imin(E, cols - c)) : 0);
+        }
+    });
+    const Raw8<T> e = own_units(v, lds_units[U > 1 ? tid >> 6 : 0]);
+    const int64_t r = r0 + tid / kRowLanes, b = c0 / kMx4Block + lq / 4, nb = (cols + kMx4Block - 1) / kMx4Block;
     if (r >= rows || b >= nb) return;   // whole quads
-    Raw8<T> v;
-    with_past(on16(x) && ldx * sizeof(T) % 16 == 0,
-              [&](auto past) { load8<past>(v, x + r * ldx + c, (int)imax(0, imin(8, cols - c))); });
     uint32_t s;
-    const uint32_t code = encode8<STOCHASTIC>(v, STOCHASTIC ? *seed_at : 0, 4 * (uint64_t)(r * nb + b) + (lq & 3), 0, &s);
+    const uint32_t code = encode8<STOCHASTIC>(e, STOCHASTIC ? *seed_at : 0, 4 * (uint64_t)(r * nb + b) + (lq & 3), 0, &s);
     *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
     if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
 }
 
+// Back: a lane takes a unit of U rows of the tile.
 template <class T>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
                                                                   int64_t ldo, uint32_t tiles_x) {
+    constexpr int U = kUnits<T>, E = kUnit<T>, kRowUnits = kRowTileCols / E;
     const uint32_t id = tile_run(blockIdx.x, gridDim.x);
-    const int64_t r = (int64_t)(id / tiles_x) * kRowTileRows + threadIdx.x / kRowLanes;
-    const int64_t c = (int64_t)(id % tiles_x) * kRowTileCols + 8 * (threadIdx.x % kRowLanes);
-    if (r >= rows || c >= cols) return;
-    int64_t code, scale;
-    m.row((uint32_t)r, &code, &scale);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(m.codes + code + c / 2);
-    const float f = scale_value(m.scales[scale + c / kMx4Block]);
-    with_past(sizeof(T) == 2 && on16(out) && ldo * sizeof(T) % 16 == 0,
-              [&](auto past) { store8<past>(out + r * ldo + c, w, f, (int)imin(8, cols - c)); });
+    const int64_t r0 = (int64_t)(id / tiles_x) * kRowTileRows + threadIdx.x / kRowUnits;
+    const int64_t c = (int64_t)(id % tiles_x) * kRowTileCols + E * (threadIdx.x % kRowUnits);
+    if (c >= cols) return;
+    uint32_t w[U], s[U];
+#pragma unroll
+    for (int h = 0; h < U; ++h) {
+        const int64_t r = r0 + h * (kRowTileRows / U);
+        if (r < rows) {
+            int64_t code, scale;
+            m.row((uint32_t)r, &code, &scale);
+            w[h] = unit_codes<T>(m.codes + code, c / E);
+            s[h] = ld(m.scales + scale + c / kMx4Block);
+        }
+    }
+    with_past(on16(out) && ldo * sizeof(T) % 16 == 0, [&](auto past) {
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+            const int64_t r = r0 + h * (kRowTileRows / U);
+            if (r < rows) store_unit<past>(out + r * ldo + c, decode_unit(T{}, w[h], scale_value(s[h])), (int)imin(E, cols - c));
+        }
+    });
 }
 
 // Along columns, with or without rows: a workgroup takes 128 by 128 elements.
@@ -256,6 +298,7 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
                                                                      int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
                                                                      Mx4Out by_col, const uint64_t *__restrict__ seed_at) {
     constexpr int kCols = kColTileCols<T>, kColLanes = kCols / 8, kColSteps = kColTileRows * kColLanes / kThreads;
+    constexpr int U = kUnits<T>, E = kUnit<T>, kRowUnits = kCols / E;
     constexpr int kColBlocks = kColTileRows / kMx4Block;   // of a column
     // Bytes of a row in LDS, and more between blocks of them: neither the writes of rows nor the reads of four blocks'
     // words by the lanes of a quad meet in a bank.
@@ -266,20 +309,21 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
     const int64_t r0 = (int64_t)(id / tiles_x) * kColTileRows, c0 = (int64_t)(id % tiles_x) * kCols;
     const uint64_t seed = STOCHASTIC ? *seed_at : 0;
     const int64_t nbr = (cols + kMx4Block - 1) / kMx4Block, nbc = (rows + kMx4Block - 1) / kMx4Block;
-    Raw8<T> v[kColSteps];
+    u32x4 v[kColSteps * U];
     with_past(on16(x) && ldx * sizeof(T) % 16 == 0, [&](auto past) {
 #pragma unroll
-        for (int i = 0; i < kColSteps; ++i) {
+        for (int i = 0; i < kColSteps * U; ++i) {
             const int q = i * kThreads + threadIdx.x;
-            const int64_t r = r0 + q / kColLanes, c = c0 + 8 * (q % kColLanes);
-            load8<past>(v[i], x + r * ldx + c, r < rows ? (int)imax(0, imin(8, cols - c)) : 0);
+            const int64_t r = r0 + q / kRowUnits, c = c0 + E * (q % kRowUnits);
+            v[i] = load_unit<past>(x + r * ldx + c, r < rows ? (int)imax(0, imin(E, cols - c)) : 0);
         }
     });
 #pragma unroll
-    for (int i = 0; i < kColSteps; ++i) {
-        const int q = i * kThreads + threadIdx.x, lr = q / kColLanes, lq = q % kColLanes;
-        __builtin_memcpy(__builtin_assume_aligned(lds_row(lr) + lq * sizeof v[i], 16), &v[i], sizeof v[i]);
+    for (int i = 0; i < kColSteps * U; ++i) {
+        const int q = i * kThreads + threadIdx.x;
+        *reinterpret_cast<u32x4 *>(lds_row(q / kRowUnits) + q % kRowUnits * 16) = v[i];
     }
+    if (U > 1) __syncthreads();   // a lane's eights come from LDS
     if (ROWS) {
         constexpr int kStep = kThreads / kColLanes;   // rows between a lane's loads
         const int lq = threadIdx.x % kColLanes;
@@ -289,8 +333,11 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
         uint64_t group = 4 * (uint64_t)(r1 * nbr + b) + (lq & 3);
 #pragma unroll
         for (int i = 0; i < kColSteps; ++i) {
+            Raw8<T> e;
+            if (U == 1) __builtin_memcpy(&e, &v[i], 16);
+            else __builtin_memcpy(&e, __builtin_assume_aligned(lds_row(i * kStep + threadIdx.x / kColLanes) + lq * sizeof e, 16), sizeof e);
             uint32_t s;
-            const uint32_t code = encode8<STOCHASTIC>(v[i], seed, group, 0, &s);
+            const uint32_t code = encode8<STOCHASTIC>(e, seed, group, 0, &s);
             if (r1 + i * kStep < rows && b < nbr) {
                 *reinterpret_cast<uint32_t *>(codes) = code;
                 if ((lq & 3) == 0) *scales = (uint8_t)s;
@@ -300,7 +347,7 @@ __global__ __launch_bounds__(kThreads) void quantize_cols_mx4_kernel(int64_t row
             group += 4 * kStep * (uint64_t)nbr;
         }
     }
-    __syncthreads();
+    if (U == 1) __syncthreads();
     constexpr int kWide = 4 / sizeof(T);   // columns a lane
     static_assert(kCols / kWide * kColBlocks == kThreads, "a lane takes the blocks of one word's columns");
     const int lb = threadIdx.x % kColBlocks, lc = threadIdx.x / kColBlocks;   // a quad's codes follow each other

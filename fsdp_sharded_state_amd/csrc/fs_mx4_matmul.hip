@@ -217,14 +217,6 @@ __device__ __forceinline__ int hidden(int x) {
     return x;
 }
 
-// The lanes of a wave meet, their LDS accesses before this place before those
-// after it.  (The hardware keeps a wave's LDS accesses in order; this keeps the compiler to it.)
-__device__ __forceinline__ void wave_meets() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-}
-
 // Waits until no more than N of this wave's loads are on their way and its LDS
 // accesses are done, then for every wave.  One piece of assembly, as the fence of __syncthreads
 // would wait for every load into LDS, the steps still to come among them.
