@@ -86,6 +86,36 @@ def test_quantize(rows, cols, dtype):
             c.check(*ref.encode_matrix(v.T, bits, 1))
 
 
+@pytest.mark.parametrize("rows,cols,pad", [(8200, 1100, 0), (300, 33000, 5), (70000, 33, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("seed", [None, 7])
+def test_quantize_and_back_of_many_tiles(rows, cols, pad, dtype, seed):
+    """Rows alone, and both ways: every block of some rows and columns, and all of them against each other."""
+    say(f"many tiles {rows} {cols} {pad} {dtype} {seed}")
+    x = _values((rows, cols + pad), dtype, rows)[:, :cols]
+    alone, both, col = Guard(rows, cols), Guard(rows, cols), Guard(cols, rows)
+    sd = None if seed is None else _seed(seed)
+    fs.fs_mx4_quantize(x, alone.m, seed=sd)
+    fs.fs_mx4_quantize(x, both.m, col.m, seed=sd)
+    out = torch.full((rows, cols + pad), 7.0, device="cuda")
+    fs.fs_mx4_dequantize(alone.m, out[:, :cols])
+    assert torch.equal(alone.c, both.c) and torch.equal(alone.s, both.s)
+    assert (out[:, cols:] == 7).all()
+    for q, v, n, o in ((alone, x, cols, 0), (col, x.T, rows, 1)):
+        take = sorted({0, 1, 17, q.rows // 2, q.rows - 16, q.rows - 1})
+        c, s = q.c[take].cpu().numpy(), q.s[take].cpu().numpy()
+        nb, host = ref.blocks(n), _f64(v[take])
+        full = np.zeros((len(take), nb * ref.BLOCK))
+        full[:, :n] = host
+        index = (np.array(take)[:, None] * nb + np.arange(nb)).reshape(-1)
+        wc, ws = ref.encode(full.reshape(-1, ref.BLOCK), seed, index, o)
+        assert np.array_equal(c, wc.reshape(len(take), -1)) and np.array_equal(s, ws.reshape(len(take), -1))
+        if o == 0:
+            assert np.array_equal(_f64(out[take][:, :cols]), _decoded(q.c[take], q.s[take], cols))
+    for q in (alone, both, col):
+        q.check(q.c.cpu().numpy().copy(), q.s.cpu().numpy().copy())    # the canaries between
+
+
 @pytest.mark.parametrize("seed", [None, 99])
 def test_quantize_every_bf16_value(seed):
     """Each value beside a maximum of its own binade, of 1 to 7 binades more, and alone."""
