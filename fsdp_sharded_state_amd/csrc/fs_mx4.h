@@ -1,7 +1,7 @@
 // fs_mx4.h -- the microscaled 4-bit block format as the kernels of both MX4
 // sources make and read it.  Not part of the public ABI.
 //
-// A lane works on 8 consecutive elements: 4 bytes of codes, a quarter of a
+// A lane that quantises works on 8 consecutive elements: 4 bytes of codes, a quarter of a
 // block.  The four lanes of a quad hold one block, so its largest magnitude
 // is joined by two quad permutes and no LDS.  CDNA4 converts a pair of values
 // to codes and back, scale and rounding included, in one instruction each

@@ -20,8 +20,9 @@ constexpr int kWavesExchanging = kUnits<T> > 1 ? kThreads / 64 : 1;
 
 // ------------------------------------------------------------------ shards --
 
-// A tile's codes and scales go through LDS: 16 bytes a lane are stored for the
-// four that a lane makes at a time, and four scales for one.
+// Copy-in: a tile a workgroup, all its loads on their way before the first block is made.  Its codes and scales
+// go through LDS: 16 bytes a lane are stored for the four that a lane makes at a time, and four scales
+// for one.  HBM bounds it: one 7B block in bf16 78 us, 6.6 TB/s.
 template <class T, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
                                                             const Mx4Run *__restrict__ pads,
@@ -78,6 +79,8 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
             *reinterpret_cast<const uint32_t *>(lds_scales + 4 * tid);
 }
 
+// Copy-out: a lane makes 16 bytes of values at a time, whole cache lines a wave.  HBM bounds it: one 7B block in bf16
+// 73 us, 7.0 TB/s.
 template <class T>
 __global__ __launch_bounds__(kThreads) void unpack_mx4_kernel(const Mx4Tile *__restrict__ tiles,
                                                               const uint8_t *__restrict__ gathered,
@@ -145,10 +148,10 @@ __device__ __forceinline__ void add_slices(float (&acc)[8], const Mx4Slices &sli
     }
 }
 
-// One 7B block's shard of 8 slices takes 41.6 us in parts of tiles, three of 32 slices 296, where whole tiles took 44.3 and
-// 350, two steps at a time 48 and 295, four 53 and 302.  With the parts of a tile on one XCD, and
-// stores past the caches, 40.6 and 282.
-
+// The sums are in fp32, slice by slice.  HBM's mix of many read streams and a write bounds it: one 7B block's
+// shard of 8 slices 35.3 us, 5.9 TB/s, three of 32 slices 276, 5.8 TB/s.  In parts of tiles the two took 41.6 and 296
+// where whole tiles took 44.3 and 350, two steps of them at a time 48 and 295, four 53 and 302; with the parts of a
+// tile on one XCD and stores past the caches 40.6 and 282.
 __global__ __launch_bounds__(kThreads) void reduce_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
                                                               const Mx4Run *__restrict__ gaps, Mx4Slices slices,
                                                               int nterms, int first_pass, float divide, float scale,
@@ -207,7 +210,7 @@ __device__ __forceinline__ uint32_t tile_run(uint32_t id, uint32_t tiles) {
     return xcd * each + min(xcd, rest) + id / kXcds;
 }
 
-// Along rows alone, and back: a workgroup takes 16 rows by 128 elements, a lane 8 of them.
+// Along rows alone, and back: a tile is 16 rows by 128 elements, a lane's eight of them or a unit.
 constexpr int kRowLanes = 16, kRowTileCols = 8 * kRowLanes, kRowTileRows = kThreads / kRowLanes;
 
 // STEPS tiles side by side where there are many: their codes and scales then go through LDS, to be stored 256 and 16
@@ -265,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t row
     }
 }
 
-// Back: a lane takes a unit of U rows of the tile.
+// Back: a lane takes a unit of U rows of the tile.  HBM bounds it: 8192 by 11008 to bf16 37 us, 6.2 TB/s, to fp32 62, 6.6.
 template <class T>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
                                                                   int64_t ldo, uint32_t tiles_x) {
@@ -294,10 +297,12 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
     });
 }
 
-// Along columns, with or without rows: a workgroup takes 128 by 128 elements.
-// Its rows' blocks come straight from the loads, as above.  Its columns' come from a copy in
-// LDS, where a lane takes 32 rows of two columns (of one in fp32), two blocks of its own: reads
-// of whole rows by the wave, and no joins between lanes.
+// Along columns, with or without rows: a workgroup takes 128 rows by 256 bytes, and the columns' blocks come from a
+// copy in LDS.  There a lane takes 32 rows of a word, one or two blocks of its own, so no
+// lanes join; the lanes of a quad take the column's four blocks, which they store side by side.
+// 8192 by 11008 bf16 both ways: 66 us to nearest, 4.2 TB/s, which HBM and the LDS copy bound; 93 random, bound by the vector
+// instructions, of which the random bits' multiplications (28 for 16 elements) take several times an addition's cycles.
+// Columns alone 55 and 58.  From fp32 105 and 123, 4.3 and 3.7 TB/s.
 constexpr int kColTileRows = 128;
 template <class T>
 constexpr int kColTileCols = 256 / sizeof(T);
