@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from typing import List, Optional, Sequence
 
@@ -201,6 +202,12 @@ def _dev_ptr(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
+# What a call asks of every tensor of a list.
+_DATA_PTR, _NUMEL, _IS_CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
+_ELEMENT_SIZE, _GET_DEVICE = torch.Tensor.element_size, torch.Tensor.get_device
+_IS_CUDA, _DTYPE = operator.attrgetter("is_cuda"), operator.attrgetter("dtype")
+
+
 class Plan:
     """An uploaded-or-not layout plan (wraps fs_plan_t)."""
 
@@ -326,10 +333,11 @@ class Plan:
         return self
 
     def ptr_table(self, tensors: Sequence[torch.Tensor], what: str, elem_bytes: Optional[int] = None,
-                  numels: Optional[Sequence[int]] = None, stream=None) -> torch.Tensor:
+                  numels: Optional[Sequence[int]] = None, stream=None, known: bool = False) -> torch.Tensor:
         """Device array of the tensors' data pointers (cached per pointer set).
         Every tensor must hold `numels[i]` elements (default: its parameter's
-        element count) of `elem_bytes` bytes (default: the plan's).
+        element count) of `elem_bytes` bytes (default: the plan's).  known: the
+        caller has checked that they are GPU tensors of that element size.
 
         The kernels read the table when they run, not when they are enqueued,
         so a table must outlive every launch that uses it.  A few recent sets
@@ -344,9 +352,11 @@ class Plan:
             raise ValueError(f"{what}: expected {self.info.n_params} tensors, got {len(tensors)}")
         esz = self.info.elem_bytes if elem_bytes is None else elem_bytes
         want = self.numels if numels is None else numels
-        ptrs = [t.data_ptr() if t.numel() else 0 for t in tensors]
-        if [t.numel() for t in tensors] != list(want) or not all(
-                t.element_size() == esz and t.is_cuda and t.is_contiguous() for t in tensors):
+        ptrs, held = list(map(_DATA_PTR, tensors)), list(map(_NUMEL, tensors))   # in bulk: half the time of a loop's
+        if 0 in held:
+            ptrs = [p if n else 0 for p, n in zip(ptrs, held)]
+        if held != list(want) or not all(map(_IS_CONTIGUOUS, tensors)) or not (
+                known or all(map(_IS_CUDA, tensors)) and not set(map(_ELEMENT_SIZE, tensors)) - {esz}):
             for i, t in enumerate(tensors):     # which one it is
                 if t.element_size() != esz:
                     raise ValueError(f"{what}[{i}]: element size {t.element_size()} != {esz}")
@@ -965,11 +975,10 @@ class Mx4Plan:
     def _params(self, tensors, what: str, index: int, stream) -> tuple:
         if not tensors:
             return 0, FS_BF16
-        kinds = {(t.dtype, t.get_device()) for t in tensors}
-        if len(kinds) > 1 or tensors[0].get_device() != index:
+        if len(set(map(_DTYPE, tensors))) > 1 or set(map(_GET_DEVICE, tensors)) != {index}:
             raise ValueError(f"{what} must share one dtype, on the buffer's GPU")
         code = _dtype_code(tensors[0].dtype)
-        tab = self.plan.ptr_table(tensors, what, elem_bytes=tensors[0].element_size(), stream=stream)
+        tab = self.plan.ptr_table(tensors, what, elem_bytes=tensors[0].element_size(), stream=stream, known=True)
         return tab.data_ptr(), code
 
 
