@@ -213,23 +213,30 @@ __device__ __forceinline__ uint32_t tile_run(uint32_t id, uint32_t tiles) {
 // Along rows alone, and back: a tile is 16 rows by 128 elements, a lane's eight of them or a unit.
 constexpr int kRowLanes = 16, kRowTileCols = 8 * kRowLanes, kRowTileRows = kThreads / kRowLanes;
 
-// STEPS tiles side by side where there are many: their codes and scales then go through LDS, to be stored 256 and 16
-// bytes a row.  8192 by 11008 bf16 44.7 us for 49.6 a tile at a time, random 62.5 for 67.9; 4096 by 4096 8.5 for 9.7; 2048
-// by 4096 5.2 for 5.2; 1024 by 4096 3.8 for 3.3, 16 by 4096 2.4 for 1.8.
+// STEPS tiles of the row-major order, one after the other, where there are many: their codes and scales then go through
+// LDS, to be stored 16 bytes and one a lane.  Past 4096 tiles 8192 by 11008 bf16 takes 44 us for 50 a tile at a time, random
+// 59 to 64 for 67, 1.25M by 32 46 for 65, 4096 by 4096 8.6 for 9.7; 2048 by 4096 takes 5.2 either way, 1024 by 4096 3.8
+// for 3.3 and 16 by 4096 2.4 for 1.8.
 constexpr int kManySteps = 4;
 constexpr int64_t kManyTiles = 4096;
 template <class T, bool STOCHASTIC, int STEPS>
 __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t rows, int64_t cols, const T *__restrict__ x,
                                                                      int64_t ldx, uint32_t tiles_x, Mx4Out by_row,
                                                                      const uint64_t *__restrict__ seed_at) {
-    constexpr int U = kUnits<T>, E = kUnit<T>, kRowUnits = kRowTileCols / E, kCols = STEPS * kRowTileCols;
+    constexpr int U = kUnits<T>, E = kUnit<T>, kRowUnits = kRowTileCols / E, kTileBlocks = kRowTileCols / kMx4Block;
     __shared__ u32x4 lds_units[kWavesExchanging<T>][128];
-    __shared__ __attribute__((aligned(16))) uint32_t lds_codes[kRowTileRows][kCols / 8];
-    __shared__ uint8_t lds_scales[kRowTileRows][kCols / kMx4Block];
-    const uint32_t id = tile_run(blockIdx.x, gridDim.x);
+    __shared__ __attribute__((aligned(16))) uint32_t lds_codes[kRowTileRows][STEPS * kRowLanes];
+    __shared__ uint8_t lds_scales[kRowTileRows][STEPS * kTileBlocks];
+    const uint32_t first = tile_run(blockIdx.x, gridDim.x) * STEPS;
     const int tid = threadIdx.x, lr = tid / kRowLanes, lq = tid % kRowLanes;
-    const int64_t r0 = (int64_t)(id / tiles_x) * kRowTileRows, c0 = (int64_t)(id % tiles_x) * kCols;
-    const int64_t r = r0 + lr, b = c0 / kMx4Block, nb = (cols + kMx4Block - 1) / kMx4Block;
+    const int64_t nb = (cols + kMx4Block - 1) / kMx4Block;
+    uint32_t ty[STEPS], tx[STEPS];   // tiles beyond the last one lie below the matrix
+    ty[0] = first / tiles_x, tx[0] = first % tiles_x;
+#pragma unroll
+    for (int i = 1; i < STEPS; ++i) {
+        const bool wrap = tx[i - 1] + 1 == tiles_x;
+        ty[i] = ty[i - 1] + wrap, tx[i] = wrap ? 0 : tx[i - 1] + 1;
+    }
     u32x4 v[STEPS][U];
     with_past(on16(x) && ldx * sizeof(T) % 16 == 0, [&](auto past) {
 #pragma unroll
@@ -237,34 +244,35 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t row
 #pragma unroll
             for (int h = 0; h < U; ++h) {
                 const int u = (tid & ~63) * U + 64 * h + (tid & 63);
-                const int64_t row = r0 + u / kRowUnits, c = c0 + i * kRowTileCols + E * (u % kRowUnits);
-                v[i][h] = load_unit<past>(x + row * ldx + c, row < rows ? (int)imax(0, imin(E, cols - c)) : 0);
+                const int64_t r = (int64_t)ty[i] * kRowTileRows + u / kRowUnits, c = (int64_t)tx[i] * kRowTileCols + E * (u % kRowUnits);
+                v[i][h] = load_unit<past>(x + r * ldx + c, r < rows ? (int)imax(0, imin(E, cols - c)) : 0);
             }
     });
-    const uint64_t seed = STOCHASTIC ? *seed_at : 0, group = 4 * (uint64_t)(r * nb + b) + lq;
+    const uint64_t seed = STOCHASTIC ? *seed_at : 0;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         const Raw8<T> e = own_units(v[i], lds_units[U > 1 ? tid >> 6 : 0]);
+        const int64_t r = (int64_t)ty[i] * kRowTileRows + lr, b = (int64_t)tx[i] * kTileBlocks + lq / 4;
         uint32_t s;
-        const uint32_t code = encode8<STOCHASTIC>(e, seed, group + i * kRowLanes, 0, &s);
-        const int q = i * kRowLanes + lq;
+        const uint32_t code = encode8<STOCHASTIC>(e, seed, 4 * (uint64_t)(r * nb + b) + (lq & 3), 0, &s);
         if (STEPS > 1) {
-            lds_codes[lr][q] = code;
-            if ((q & 3) == 0) lds_scales[lr][q / 4] = (uint8_t)s;
-        } else if (r < rows && b + q / 4 < nb) {
-            *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * q) = code;
-            if ((q & 3) == 0) by_row.scales[r * by_row.scale_stride + b + q / 4] = (uint8_t)s;
+            lds_codes[lr][i * kRowLanes + lq] = code;
+            if ((lq & 3) == 0) lds_scales[lr][i * kTileBlocks + lq / 4] = (uint8_t)s;
+        } else if (r < rows && b < nb) {
+            *reinterpret_cast<uint32_t *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes + 4 * (lq & 3)) = code;
+            if ((lq & 3) == 0) by_row.scales[r * by_row.scale_stride + b] = (uint8_t)s;
         }
     }
     if (STEPS == 1) return;
     __syncthreads();
-    constexpr int kBlocks = kCols / kMx4Block;
-    static_assert(STEPS == 1 || kBlocks * kRowTileRows == kThreads, "a thread for every block");
-    const int row = tid / kBlocks, at = tid % kBlocks;
-    if (r0 + row < rows && b + at < nb) {
-        *reinterpret_cast<u32x4 *>(by_row.codes + (r0 + row) * by_row.code_stride + (b + at) * kMx4BlockBytes) =
+    static_assert(STEPS == 1 || STEPS * kTileBlocks * kRowTileRows == kThreads, "a thread for every block");
+    const int row = tid / (STEPS * kTileBlocks), at = tid % (STEPS * kTileBlocks);
+    const uint32_t tile = first + at / kTileBlocks;
+    const int64_t r = (int64_t)(tile / tiles_x) * kRowTileRows + row, b = (int64_t)(tile % tiles_x) * kTileBlocks + at % kTileBlocks;
+    if (r < rows && b < nb) {
+        *reinterpret_cast<u32x4 *>(by_row.codes + r * by_row.code_stride + b * kMx4BlockBytes) =
             *reinterpret_cast<const u32x4 *>(&lds_codes[row][4 * at]);
-        by_row.scales[(r0 + row) * by_row.scale_stride + b + at] = lds_scales[row][at];
+        by_row.scales[r * by_row.scale_stride + b] = lds_scales[row][at];
     }
 }
 
@@ -701,8 +709,7 @@ extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dty
                         : mat_tiles(what, rows, cols, kRowTileRows, kRowTileCols, &across, &tiles))
         return rc;
     const bool many = !by_col && tiles > kManyTiles;
-    if (many)   // fewer than they were
-        if (int rc = mat_tiles(what, rows, cols, kRowTileRows, kManySteps * kRowTileCols, &across, &tiles)) return rc;
+    if (many) tiles = (tiles + kManySteps - 1) / kManySteps;
     if (tiles == 0) return FS_OK;
     (void)hipGetLastError();
     by_type(dtype, seed != nullptr, [&](auto t, auto stochastic) {
