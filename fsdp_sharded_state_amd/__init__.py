@@ -946,8 +946,15 @@ class Mx4Plan:
         self.close()
 
     def upload(self, device="cuda", stream=None) -> "Mx4Plan":
-        ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=device)
-        _launch(ws.get_device(), stream, lib().fs_mx4_plan_upload, self._h, ws.data_ptr(), ws.numel())
+        """Put the tables on a GPU.  They do not change, so where they are there already they stay."""
+        where = torch.device(device)
+        if where.type != "cuda":
+            raise ValueError(f"fs_mx4_plan: the tables go to a GPU, not to {where}")
+        index = torch.cuda.current_device() if where.index is None else where.index
+        if self.workspace is not None and self.workspace.get_device() == index:
+            return self
+        ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=torch.device("cuda", index))
+        _launch(index, stream, lib().fs_mx4_plan_upload, self._h, ws.data_ptr(), ws.numel())
         if self.workspace is not None:
             self._earlier.append(self.workspace)
         self.workspace = ws

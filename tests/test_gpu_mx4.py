@@ -811,6 +811,8 @@ def test_refusals_on_the_gpu():
                      (dict(ptrs=(O, None)), fs.FS_E_INVAL), (dict(ptrs=(O, O + 8)), fs.FS_E_ALIGN), (dict(out=None), fs.FS_E_INVAL),
                      (dict(out=P + 2), fs.FS_E_ALIGN), (dict(out=O + 64), fs.FS_E_INVAL)):
         assert reduce(**kw) == code
+    ws = mp.workspace
+    assert mp.upload().workspace is ws and mp.upload(device=ws.device).workspace is ws      # there already
     host = torch.empty(1 << 12, dtype=torch.uint8)
     assert L.fs_mx4_plan_upload(mp._h, (host.data_ptr() + 15) & ~15, 3000, None) == fs.FS_E_INVAL
     with pytest.raises(ValueError, match="no longer"):

@@ -225,6 +225,8 @@ def test_binding_refusals():
         fs.fs_pack_mx4(mp, [torch.zeros(8, 64)], torch.zeros(5, dtype=torch.uint8))
     with pytest.raises(ValueError, match="GPU"):
         fs.fs_pack_mx4(mp, [torch.zeros(8, 64)], torch.zeros(mp.gathered_bytes, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="GPU, not to cpu"):
+        mp.upload(device="cpu")
     with pytest.raises(ValueError, match="slices"):
         fs.fs_reduce_shard_mx4(mp, [], torch.zeros(4 * 64), rank=0)
     with pytest.raises(ValueError, match="float32"):
