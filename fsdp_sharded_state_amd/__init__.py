@@ -202,6 +202,42 @@ def _dev_ptr(t: torch.Tensor, what: str) -> int:
     return t.data_ptr()
 
 
+def _bytes_on(index: int, stream, handle: int, nbytes: int) -> torch.Tensor:
+    """Memory of the current GPU, `index`, that belongs to a stream (None: the
+    current one): the allocator hands it out again in that stream's order."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    device = torch.device("cuda", index)
+    own = (stream if isinstance(stream, torch.cuda.Stream) else
+           torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
+    with torch.cuda.stream(own):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _upload(fn, plan, nbytes: int, device, stream) -> torch.Tensor:
+    """The tables of a plan on a GPU, in memory of the stream that copies them:
+    what another stream has under way could still write to memory of its own.
+    In place of the per-thread default stream, which the allocator cannot tell
+    from other threads', the default one copies; the copy is waited for."""
+    where, nbytes = torch.device(device), max(16, nbytes)
+    if where.type != "cuda":
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=where)
+        _check(fn(plan, ws.data_ptr(), nbytes, None))   # refuses host memory
+        return ws
+    index = torch.cuda.current_device() if where.index is None else where.index
+    if index != torch._C._cuda_getDevice():
+        with torch.cuda.device(index):
+            return _upload(fn, plan, nbytes, where, stream)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tables go to {torch.device('cuda', index)}")
+    if handle == _PER_THREAD_STREAM:
+        stream, handle = torch.cuda.default_stream(index), 0
+    ws = _bytes_on(index, stream, handle, nbytes)
+    _check(fn(plan, ws.data_ptr(), nbytes, handle))
+    return ws
+
+
 # What a call asks of every tensor of a list.
 _DATA_PTR, _NUMEL, _IS_CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous
 _ELEMENT_SIZE, _GET_DEVICE = torch.Tensor.element_size, torch.Tensor.get_device
@@ -327,9 +363,8 @@ class Plan:
                                    _dev_ptr(shard, "shard") if shard.numel() else 0, _stream(stream)))
 
     def upload(self, device="cuda", stream=None) -> "Plan":
-        ws = torch.empty(max(16, self.info.workspace_bytes), dtype=torch.uint8, device=device)
-        _check(lib().fs_plan_upload(self._h, ws.data_ptr(), ws.numel(), _stream(stream)))
-        self.workspace = ws
+        """Put the tables on a GPU, copied on `stream`, and wait for them."""
+        self.workspace = _upload(lib().fs_plan_upload, self._h, self.info.workspace_bytes, device, stream)
         return self
 
     def ptr_table(self, tensors: Sequence[torch.Tensor], what: str, elem_bytes: Optional[int] = None,
@@ -428,9 +463,8 @@ class Reshard:
         self.close()
 
     def upload(self, device="cuda", stream=None) -> "Reshard":
-        ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=device)
-        _check(lib().fs_reshard_upload(self._h, ws.data_ptr(), ws.numel(), _stream(stream)))
-        self.workspace = ws
+        """Put the tables on a GPU, copied on `stream`, and wait for them."""
+        self.workspace = _upload(lib().fs_reshard_upload, self._h, self.workspace_bytes, device, stream)
         return self
 
 
@@ -707,14 +741,7 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
         raise ValueError("the per-thread default stream cannot be used here: make a stream for each thread")
     if scratch == 0:
         return _check(fn(*args, None, 0, handle))
-    if stream is None:
-        ws = torch.empty(scratch, dtype=torch.uint8, device=index)
-    else:
-        device = torch.device("cuda", index)
-        own = (stream if isinstance(stream, torch.cuda.Stream) else
-               torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
-        with torch.cuda.stream(own):
-            ws = torch.empty(scratch, dtype=torch.uint8, device=device)
+    ws = _bytes_on(index, stream, handle, scratch)
     return _check(fn(*args, ws.data_ptr(), scratch, handle))
 
 
@@ -953,8 +980,7 @@ class Mx4Plan:
         index = torch.cuda.current_device() if where.index is None else where.index
         if self.workspace is not None and self.workspace.get_device() == index:
             return self
-        ws = torch.empty(max(16, self.workspace_bytes), dtype=torch.uint8, device=torch.device("cuda", index))
-        _launch(index, stream, lib().fs_mx4_plan_upload, self._h, ws.data_ptr(), ws.numel())
+        ws = _upload(lib().fs_mx4_plan_upload, self._h, self.workspace_bytes, torch.device("cuda", index), stream)
         if self.workspace is not None:
             self._earlier.append(self.workspace)
         self.workspace = ws
