@@ -214,7 +214,41 @@ def _bytes_on(index: int, stream, handle: int, nbytes: int) -> torch.Tensor:
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _upload(fn, plan, nbytes: int, device, stream) -> torch.Tensor:
+class _Table:
+    """Device memory that kernels read when they run, not when they are
+    enqueued.  The allocator hands it out again in the order of the stream it
+    was taken on; every other stream that reads it is recorded, once, so that
+    the allocator waits for that one too."""
+
+    def __init__(self, memory: torch.Tensor, handle: int):
+        self.memory = memory
+        self._known = {handle}
+
+    def read_on(self, stream, handle: int) -> bool:
+        """A launch on `stream` (None: the current one), whose handle this is,
+        reads the memory.  False where the allocator cannot be told: a bare
+        handle may be destroyed before the memory is given back, and the
+        per-thread default stream is another one in every thread."""
+        if handle in self._known:
+            return True
+        if stream is None:
+            stream = torch.cuda.current_stream(self.memory.device)
+        if handle == _PER_THREAD_STREAM or not isinstance(stream, torch.cuda.Stream):
+            return False
+        self.memory.record_stream(stream)
+        self._known.add(handle)
+        return True
+
+
+def _read_on(table: Optional[_Table], stream) -> Optional[int]:
+    """The handle of the stream of a launch that reads a plan's tables (None: it has none yet, which the call refuses)."""
+    handle = _stream(stream)
+    if table is not None:
+        table.read_on(stream, handle)
+    return handle
+
+
+def _upload(fn, plan, nbytes: int, device, stream) -> _Table:
     """The tables of a plan on a GPU, in memory of the stream that copies them:
     what another stream has under way could still write to memory of its own.
     In place of the per-thread default stream, which the allocator cannot tell
@@ -223,7 +257,7 @@ def _upload(fn, plan, nbytes: int, device, stream) -> torch.Tensor:
     if where.type != "cuda":
         ws = torch.empty(nbytes, dtype=torch.uint8, device=where)
         _check(fn(plan, ws.data_ptr(), nbytes, None))   # refuses host memory
-        return ws
+        return _Table(ws, 0)
     index = torch.cuda.current_device() if where.index is None else where.index
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
@@ -235,7 +269,7 @@ def _upload(fn, plan, nbytes: int, device, stream) -> torch.Tensor:
         stream, handle = torch.cuda.default_stream(index), 0
     ws = _bytes_on(index, stream, handle, nbytes)
     _check(fn(plan, ws.data_ptr(), nbytes, handle))
-    return ws
+    return _Table(ws, handle)
 
 
 # What a call asks of every tensor of a list.
@@ -245,7 +279,10 @@ _IS_CUDA, _DTYPE = operator.attrgetter("is_cuda"), operator.attrgetter("dtype")
 
 
 class Plan:
-    """An uploaded-or-not layout plan (wraps fs_plan_t)."""
+    """An uploaded-or-not layout plan (wraps fs_plan_t).  Keep a plan until the
+    work of calls on a bare stream handle is done, and as long as a captured
+    graph holds calls on it; for other streams the tables stay as long as
+    enqueued work reads them."""
 
     def __init__(self, handle: int):
         self._h = ctypes.c_void_p(handle)
@@ -254,6 +291,7 @@ class Plan:
         _check(lib().fs_plan_info(self._h, ctypes.byref(info)))
         self.info = info
         self.workspace: Optional[torch.Tensor] = None
+        self._table: Optional[_Table] = None    # the workspace and who reads it
         self._ptr_cache = {}
         self._pinned = set()        # pointer-table keys a captured graph or another stream may still read
         self._pieces = {}           # rank -> local piece element counts
@@ -360,11 +398,12 @@ class Plan:
                 raise ValueError(f"local tensor {i}: {t.numel()} elements, rank {rank} holds {n}")
         tab = self.ptr_table(tensors, "local tensors", numels=want, stream=stream)
         _check(lib().fs_load_local(self._h, int(rank), tab.data_ptr(),
-                                   _dev_ptr(shard, "shard") if shard.numel() else 0, _stream(stream)))
+                                   _dev_ptr(shard, "shard") if shard.numel() else 0, _read_on(self._table, stream)))
 
     def upload(self, device="cuda", stream=None) -> "Plan":
         """Put the tables on a GPU, copied on `stream`, and wait for them."""
-        self.workspace = _upload(lib().fs_plan_upload, self._h, self.info.workspace_bytes, device, stream)
+        self._table = _upload(lib().fs_plan_upload, self._h, self.info.workspace_bytes, device, stream)
+        self.workspace = self._table.memory
         return self
 
     def ptr_table(self, tensors: Sequence[torch.Tensor], what: str, elem_bytes: Optional[int] = None,
@@ -453,6 +492,7 @@ class Reshard:
         _check(lib().fs_reshard_info(h, ctypes.byref(wb), ctypes.byref(ns)))
         self.workspace_bytes, self.n_segments = wb.value, ns.value
         self.workspace: Optional[torch.Tensor] = None
+        self._table: Optional[_Table] = None    # the workspace and who reads it
 
     def close(self):
         h = self.__dict__.pop("_h", None)
@@ -464,7 +504,8 @@ class Reshard:
 
     def upload(self, device="cuda", stream=None) -> "Reshard":
         """Put the tables on a GPU, copied on `stream`, and wait for them."""
-        self.workspace = _upload(lib().fs_reshard_upload, self._h, self.workspace_bytes, device, stream)
+        self._table = _upload(lib().fs_reshard_upload, self._h, self.workspace_bytes, device, stream)
+        self.workspace = self._table.memory
         return self
 
 
@@ -479,7 +520,7 @@ def fs_reshard(r: Reshard, src_gathered: torch.Tensor, dst_gathered: torch.Tenso
         raise ValueError("fs_reshard: buffer sizes do not match the plans")
     _check(lib().fs_reshard(r._h, _dev_ptr(src_gathered, "src_gathered") if src_gathered.numel() else 0,
                             _dev_ptr(dst_gathered, "dst_gathered") if dst_gathered.numel() else 0,
-                            _stream(stream)))
+                            _read_on(r._table, stream)))
 
 
 def fs_pack(plan: Plan, params: Sequence[torch.Tensor], out: torch.Tensor, rank: int = -1, stream=None):
@@ -488,7 +529,8 @@ def fs_pack(plan: Plan, params: Sequence[torch.Tensor], out: torch.Tensor, rank:
     if out.numel() != want or out.element_size() != plan.info.elem_bytes:
         raise ValueError(f"fs_pack: out must hold {want} elements of {plan.info.elem_bytes} bytes")
     tab = plan.ptr_table(params, "params", stream=stream)
-    _check(lib().fs_pack(plan._h, tab.data_ptr(), _dev_ptr(out, "out") if want else 0, int(rank), _stream(stream)))
+    _check(lib().fs_pack(plan._h, tab.data_ptr(), _dev_ptr(out, "out") if want else 0, int(rank),
+                         _read_on(plan._table, stream)))
 
 
 def fs_pack_cast(plan: Plan, params: Sequence[torch.Tensor], out: torch.Tensor, rank: int = -1, stream=None):
@@ -504,7 +546,7 @@ def fs_pack_cast(plan: Plan, params: Sequence[torch.Tensor], out: torch.Tensor, 
         raise ValueError("fs_pack_cast: parameters must share one dtype")
     tab = plan.ptr_table(params, "params", elem_bytes=params[0].element_size(), stream=stream)
     _check(lib().fs_pack_cast(plan._h, tab.data_ptr(), _dtype_code(dt), _dev_ptr(out, "out") if want else 0,
-                              int(rank), _stream(stream)))
+                              int(rank), _read_on(plan._table, stream)))
 
 
 def fs_unpack(plan: Plan, gathered: torch.Tensor, params: Sequence[torch.Tensor], stream=None):
@@ -513,7 +555,7 @@ def fs_unpack(plan: Plan, gathered: torch.Tensor, params: Sequence[torch.Tensor]
         raise ValueError("fs_unpack: gathered has the wrong size or element size")
     tab = plan.ptr_table(params, "params", stream=stream)
     _check(lib().fs_unpack(plan._h, _dev_ptr(gathered, "gathered") if gathered.numel() else 0,
-                           tab.data_ptr(), _stream(stream)))
+                           tab.data_ptr(), _read_on(plan._table, stream)))
 
 
 def fs_reduce_shard(slices: Sequence[torch.Tensor], out: torch.Tensor, world: int, grad_acc: int = 1, stream=None):
@@ -718,9 +760,11 @@ def _scalar_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, index: Optional[i
     return t.data_ptr()
 
 
-def _launch(index: int, stream, fn, *args, scratch: int = -1):
+def _launch(index: int, stream, fn, *args, scratch: int = -1, table: Optional[_Table] = None):
     """Run a launching call with GPU `index` current, on `stream` (default:
-    that GPU's current stream).  scratch >= 0: that many workspace bytes and
+    that GPU's current stream).  table: what the call reads of a plan (None
+    also where a plan has none yet, which the call refuses).  scratch >= 0:
+    that many workspace bytes and
     their count go before the stream; they belong to the stream the kernels
     run on, so the allocator hands them out again in that stream's order.  The
     per-thread default stream is refused there: it is a stream of its own in
@@ -728,13 +772,15 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1):
     thread's workspace to another while it is in use."""
     if index != torch._C._cuda_getDevice():
         with torch.cuda.device(index):
-            return _launch(index, stream, fn, *args, scratch=scratch)
+            return _launch(index, stream, fn, *args, scratch=scratch, table=table)
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
     else:
         handle = _stream(stream)
         if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    if table is not None:
+        table.read_on(stream, handle)
     if scratch < 0:
         return _check(fn(*args, handle))
     if handle == _PER_THREAD_STREAM:
@@ -949,7 +995,8 @@ def fs_mx4_matmul(a: Mx4Matrix, b: Mx4Matrix, out: torch.Tensor, *, stream=None)
 
 
 class Mx4Plan:
-    """The layout of a group's quantised shards (wraps fs_mx4_plan_t)."""
+    """The layout of a group's quantised shards (wraps fs_mx4_plan_t).  To be
+    kept like a Plan."""
 
     def __init__(self, plan: Plan):
         h = ctypes.c_void_p()
@@ -962,7 +1009,8 @@ class Mx4Plan:
         self.shard_blocks, self.shard_bytes = info.shard_blocks, info.shard_bytes
         self.gathered_bytes, self.workspace_bytes = info.gathered_bytes, info.workspace_bytes
         self.workspace: Optional[torch.Tensor] = None
-        self._earlier: list = []    # workspaces of earlier uploads, which launches and captured graphs may still read
+        self._table: Optional[_Table] = None    # the workspace and who reads it
+        self._earlier: list = []    # of earlier uploads, which launches and captured graphs may still read
 
     def close(self):
         h = self.__dict__.pop("_h", None)
@@ -980,10 +1028,10 @@ class Mx4Plan:
         index = torch.cuda.current_device() if where.index is None else where.index
         if self.workspace is not None and self.workspace.get_device() == index:
             return self
-        ws = _upload(lib().fs_mx4_plan_upload, self._h, self.workspace_bytes, torch.device("cuda", index), stream)
-        if self.workspace is not None:
-            self._earlier.append(self.workspace)
-        self.workspace = ws
+        table = _upload(lib().fs_mx4_plan_upload, self._h, self.workspace_bytes, torch.device("cuda", index), stream)
+        if self._table is not None:
+            self._earlier.append(self._table)
+        self._table, self.workspace = table, table.memory
         return self
 
     def piece(self, i: int, rank: int) -> tuple:
@@ -1028,7 +1076,7 @@ def fs_pack_mx4(mp: Mx4Plan, params: Sequence[torch.Tensor], out: torch.Tensor, 
     index = out.get_device()
     tab, code = mp._params(params, "params", index, stream)
     _launch(index, stream, lib().fs_pack_mx4, mp._h, tab, code, ptr, int(rank),
-            None if seed is None else _scalar_ptr(seed, torch.int64, index, "seed"))
+            None if seed is None else _scalar_ptr(seed, torch.int64, index, "seed"), table=mp._table)
 
 
 def fs_unpack_mx4(mp: Mx4Plan, gathered: torch.Tensor, params: Sequence[torch.Tensor], *, stream=None):
@@ -1036,7 +1084,7 @@ def fs_unpack_mx4(mp: Mx4Plan, gathered: torch.Tensor, params: Sequence[torch.Te
     ptr = mp._bytes(gathered, mp.gathered_bytes, "gathered")
     index = gathered.get_device()
     tab, code = mp._params(params, "params", index, stream)
-    _launch(index, stream, lib().fs_unpack_mx4, mp._h, ptr, tab, code)
+    _launch(index, stream, lib().fs_unpack_mx4, mp._h, ptr, tab, code, table=mp._table)
 
 
 def fs_reduce_shard_mx4(mp: Mx4Plan, slices, out: torch.Tensor, *, rank: int, grad_acc: int = 1, stream=None):
@@ -1061,7 +1109,7 @@ def fs_reduce_shard_mx4(mp: Mx4Plan, slices, out: torch.Tensor, *, rank: int, gr
         if any(s.get_device() != index for s in slices):
             raise ValueError(f"fs_reduce_shard_mx4: a slice is not on {out.device}")
     _launch(index, stream, lib().fs_reduce_shard_mx4, mp._h, int(rank), int(grad_acc),
-            (ctypes.c_void_p * max(1, terms))(*ptrs), ptr)
+            (ctypes.c_void_p * max(1, terms))(*ptrs), ptr, table=mp._table)
 
 
 def fs_copy_bytes(dst: torch.Tensor, src: torch.Tensor, stream=None):

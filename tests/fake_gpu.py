@@ -28,17 +28,17 @@ class GpuTensor(torch.Tensor):
         t.pool, t.recorded = pool, []
         return t
 
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
     @classmethod
     def __torch_function__(cls, func, types, args=(), kwargs=None):
-        if func is torch.Tensor.get_device:
+        if func == torch.Tensor.get_device:
             return 0
-        if func is torch.Tensor.is_cuda.__get__:
+        if func == torch.Tensor.is_cuda.__get__:
             return True
-        if func is torch.Tensor.device.__get__:
+        if func == torch.Tensor.device.__get__:
             return torch.device("cuda", 0)
-        if func is torch.Tensor.record_stream:
-            args[0].recorded.append(args[1].cuda_stream)
-            return None
         return super().__torch_function__(func, types, args, kwargs or {})
 
 

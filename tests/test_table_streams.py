@@ -47,3 +47,63 @@ def test_tables_are_not_copied_on_the_per_thread_stream(gpu, kind, stream, curre
         p.upload(stream=stream)
     (_, args), = gpu.calls
     assert (args[3] or 0) == 0 and p.workspace.pool == 0
+
+
+def _calls():
+    """Every call that reads a plan's tables: name, and a function that makes the plan and gives (owner of the tables, call(stream))."""
+    def pack(gpu, f, dtype=torch.bfloat16, out=True, **kw):
+        p = _plan().upload()
+        params, whole = [gpu.empty(*s, dtype=dtype) for s in SHAPES], gpu.empty(p.gathered_numel)
+        return p, lambda stream: f(p, params, whole, stream=stream) if out else f(p, whole, params, stream=stream)
+
+    def mx4(gpu, call):
+        mp = fs.fs_mx4_plan(_plan()).upload()
+        params, whole = [gpu.empty(*s) for s in SHAPES], gpu.empty(mp.gathered_bytes, dtype=torch.uint8)
+        return mp, lambda stream: call(mp, params, whole, stream)
+
+    def local(gpu):
+        p = _plan().upload()
+        pieces, shard = [gpu.empty(n) for n in p.local_numels(1)], gpu.empty(p.shard_numel)
+        return p, lambda stream: p.load_local(shard, 1, pieces, stream=stream)
+
+    def reshard(gpu):
+        r = fs.fs_reshard_plan(_plan(), _plan()).upload()
+        a, b = gpu.empty(r.src_info.gathered_numel), gpu.empty(r.dst_info.gathered_numel)
+        return r, lambda stream: fs.fs_reshard(r, a, b, stream=stream)
+
+    def reduce(mp, params, whole, stream):
+        rows = whole.view(2, -1)
+        fs.fs_reduce_shard_mx4(mp, [rows[0], rows[1]], torch.empty(mp.plan.shard_numel, device="cuda"), rank=0, stream=stream)
+
+    return {"fs_pack": lambda g: pack(g, fs.fs_pack), "fs_pack_cast": lambda g: pack(g, fs.fs_pack_cast, torch.float32),
+            "fs_unpack": lambda g: pack(g, fs.fs_unpack, out=False), "fs_load_local": local, "fs_reshard": reshard,
+            "fs_pack_mx4": lambda g: mx4(g, lambda mp, ps, w, s: fs.fs_pack_mx4(mp, ps, w, stream=s)),
+            "fs_unpack_mx4": lambda g: mx4(g, lambda mp, ps, w, s: fs.fs_unpack_mx4(mp, w, ps, stream=s)),
+            "fs_reduce_shard_mx4": lambda g: mx4(g, reduce)}
+
+
+CALLS = _calls()
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_streams_that_read_a_plans_tables_are_recorded(gpu, name):
+    """Once each; a plan that goes out of scope then gives its tables back behind their work."""
+    owner, call = CALLS[name](gpu)
+    ws = owner.workspace
+
+    def launched(stream, handle):
+        call(stream)
+        assert gpu.calls[-1][0] == name and (gpu.calls[-1][1][-1] or 0) == handle
+
+    launched(None, 0)
+    launched(Stream(0), 0)
+    assert ws.recorded == []                        # the stream that they were taken on
+    for _ in range(2):
+        launched(Stream(70), 70)
+        with gpu.on(Stream(50)):
+            launched(None, 50)
+    assert ws.recorded == [70, 50]
+    with gpu.on(Stream(50)):
+        launched(Stream(0), 0)
+        launched(90, 90)                            # a bare handle may be destroyed before the plan is: the plan is to be kept
+    assert ws.recorded == [70, 50]
