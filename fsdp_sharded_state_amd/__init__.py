@@ -446,7 +446,7 @@ class Plan:
             if capturing:
                 raise RuntimeError(f"{what}: a pointer set not seen before, during graph capture; run the same "
                                    "call once before capturing so that its device pointer table exists")
-            dev = tensors[0].device if tensors else torch.device("cuda")
+            dev = next((t.device for t in tensors if t.is_cuda), torch.device("cuda"))   # one without elements may be elsewhere
             tab = torch.tensor(ptrs or [0], dtype=torch.int64, device=dev)
             if len(self._ptr_cache) >= 8:          # keep a few pointer sets (pack and unpack sides)
                 old = next((k for k in self._ptr_cache if k not in self._pinned), None)
