@@ -222,7 +222,7 @@ class _Table:
 
     def __init__(self, memory: torch.Tensor, handle: int):
         self.memory = memory
-        self._known = {handle}
+        self._known = {handle} - {_PER_THREAD_STREAM}
 
     def read_on(self, stream, handle: int) -> bool:
         """A launch on `stream` (None: the current one), whose handle this is,
@@ -416,10 +416,11 @@ class Plan:
         The kernels read the table when they run, not when they are enqueued,
         so a table must outlive every launch that uses it.  A few recent sets
         are kept; the oldest is released when a new one is made, which is safe
-        for launches on the current stream (the allocator reuses its memory in
-        stream order).  A table used while a graph is being captured, or with
-        a stream given as a raw handle, is pinned for the plan's lifetime; one
-        used on another torch stream is recorded on that stream.  A new set
+        for launches on the stream that was current when it was made (the
+        allocator reuses its memory in that stream's order); every other torch
+        stream that it is used on, given or current, is recorded.  A table used
+        while a graph is being captured, with a stream given as a raw handle or
+        on the per-thread default stream is pinned for the plan's lifetime.  A new set
         cannot be made during capture (its upload would be a captured copy
         from host memory): run the call once before capturing."""
         if len(tensors) != self.info.n_params:
@@ -448,20 +449,17 @@ class Plan:
                                    "call once before capturing so that its device pointer table exists")
             dev = next((t.device for t in tensors if t.is_cuda), torch.device("cuda"))   # one without elements may be elsewhere
             tab = torch.tensor(ptrs or [0], dtype=torch.int64, device=dev)
+            tab = _Table(tab, torch._C._cuda_getCurrentRawStream(tab.get_device()))
             if len(self._ptr_cache) >= 8:          # keep a few pointer sets (pack and unpack sides)
                 old = next((k for k in self._ptr_cache if k not in self._pinned), None)
                 if old is not None:
                     self._ptr_cache.pop(old)
             self._ptr_cache[key] = tab
-        if capturing:
+        handle = torch._C._cuda_getCurrentRawStream(tab.memory.get_device()) if stream is None else _stream(stream)
+        bare = stream is not None and not isinstance(stream, torch.cuda.Stream)
+        if not tab.read_on(stream, handle) or capturing or bare:
             self._pinned.add(key)
-        if stream is not None:
-            if isinstance(stream, torch.cuda.Stream):
-                if stream != torch.cuda.current_stream(tab.device):
-                    tab.record_stream(stream)
-            else:
-                self._pinned.add(key)
-        return tab
+        return tab.memory
 
 
 def fs_plan(shapes: Sequence[Sequence[int]], dtype="bf16", world: int = 1, use_orig_params: bool = False,

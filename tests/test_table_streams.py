@@ -107,3 +107,46 @@ def test_streams_that_read_a_plans_tables_are_recorded(gpu, name):
         launched(Stream(0), 0)
         launched(90, 90)                            # a bare handle may be destroyed before the plan is: the plan is to be kept
     assert ws.recorded == [70, 50]
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n not in ("fs_reshard", "fs_reduce_shard_mx4")])
+def test_streams_that_read_a_pointer_table_are_recorded(gpu, name):
+    """Also a table that another current stream's call has made."""
+    owner, call = CALLS[name](gpu)
+    plan = getattr(owner, "plan", owner)
+    call(None)
+    (key, held), = plan._ptr_cache.items()
+    tab = held.memory
+    assert tab.pool == 0 and tab.recorded == []
+    for _ in range(2):
+        with gpu.on(Stream(50)):
+            call(None)
+        call(Stream(70))
+    with gpu.on(Stream(70)):
+        call(Stream(0))
+    assert tab.recorded == [50, 70] and not plan._pinned
+    call(90)
+    assert tab.recorded == [50, 70] and plan._pinned == {key}
+
+
+def test_a_table_made_for_another_stream_than_the_current_one(gpu):
+    """It is filled in the current stream's order, before the call goes on, and read on the call's."""
+    plan = _plan().upload()
+    params, whole = [gpu.empty(*s) for s in SHAPES], gpu.empty(plan.gathered_numel)
+    with gpu.on(Stream(50)):
+        fs.fs_pack(plan, params, whole, stream=Stream(70))
+    (held,) = plan._ptr_cache.values()
+    assert held.memory.pool == 50 and held.memory.recorded == [70]
+    assert not plan._pinned
+    gpu.capturing = True
+    fs.fs_pack(plan, params, whole, stream=Stream(70))
+    assert len(plan._pinned) == 1
+
+
+def test_the_per_thread_stream_pins_a_table(gpu):
+    """The allocator cannot tell it from another thread's."""
+    plan = _plan().upload()
+    params, whole = [gpu.empty(*s) for s in SHAPES], gpu.empty(plan.gathered_numel)
+    with gpu.on(Stream(2)):
+        fs.fs_pack(plan, params, whole)
+    assert len(plan._pinned) == 1
