@@ -1052,13 +1052,15 @@ class Mx4Plan:
         return _dev_ptr(t, what)
 
     def _params(self, tensors, what: str, index: int, stream) -> tuple:
+        """(pointer table, its address, dtype code).  The caller holds the table until it has launched: another
+        thread's calls may release it from the plan's."""
         if not tensors:
-            return 0, FS_BF16
+            return None, 0, FS_BF16
         if len(set(map(_DTYPE, tensors))) > 1 or set(map(_GET_DEVICE, tensors)) != {index}:
             raise ValueError(f"{what} must share one dtype, on the buffer's GPU")
         code = _dtype_code(tensors[0].dtype)
         tab = self.plan.ptr_table(tensors, what, elem_bytes=tensors[0].element_size(), stream=stream, known=True)
-        return tab.data_ptr(), code
+        return tab, tab.data_ptr(), code
 
 
 def fs_mx4_plan(plan: Plan) -> Mx4Plan:
@@ -1072,7 +1074,7 @@ def fs_pack_mx4(mp: Mx4Plan, params: Sequence[torch.Tensor], out: torch.Tensor, 
     whole gathered buffer, or rank's shard).  seed: as in fs_mx4_quantize."""
     ptr = mp._bytes(out, mp.gathered_bytes if rank < 0 else mp.shard_bytes, "out")
     index = out.get_device()
-    tab, code = mp._params(params, "params", index, stream)
+    _held, tab, code = mp._params(params, "params", index, stream)
     _launch(index, stream, lib().fs_pack_mx4, mp._h, tab, code, ptr, int(rank),
             None if seed is None else _scalar_ptr(seed, torch.int64, index, "seed"), table=mp._table)
 
@@ -1081,7 +1083,7 @@ def fs_unpack_mx4(mp: Mx4Plan, gathered: torch.Tensor, params: Sequence[torch.Te
     """All-gather copy-out of 4 bits: gathered -> params (bf16 or fp32)."""
     ptr = mp._bytes(gathered, mp.gathered_bytes, "gathered")
     index = gathered.get_device()
-    tab, code = mp._params(params, "params", index, stream)
+    _held, tab, code = mp._params(params, "params", index, stream)
     _launch(index, stream, lib().fs_unpack_mx4, mp._h, ptr, tab, code, table=mp._table)
 
 

@@ -1,4 +1,7 @@
 """Where the tables of pointer sets lie, and how long.  Host side only (tests/fake_gpu.py)."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -20,3 +23,33 @@ def test_a_parameter_without_elements_may_lie_anywhere(gpu, shapes):
     tab = plan.ptr_table(params, "params")
     assert tab.is_cuda and tab.tolist() == [p.data_ptr() if p.numel() else 0 for p in params]
     assert gpu.calls[-1][0] == "fs_pack" and gpu.calls[-1][1][1] == tab.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["fs_pack", "fs_unpack", "fs_pack_cast", "fs_pack_mx4", "fs_unpack_mx4"])
+def test_a_call_holds_its_table_until_it_has_launched(gpu, monkeypatch, name):
+    """Another thread's calls on the plan may release the set between its being made and the launch."""
+    plan = fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2").upload()
+    mp = fs.fs_mx4_plan(plan).upload()
+    dtype = torch.float32 if name == "fs_pack_cast" else torch.bfloat16
+    params, whole, whole4 = [gpu.empty(8, 64, dtype=dtype)], gpu.empty(plan.gathered_numel), gpu.empty(mp.gathered_bytes, dtype=torch.uint8)
+    others = [[gpu.empty(8, 64)] for _ in range(9)]
+    alive = []
+    real = plan.ptr_table
+
+    def made(*args, **kw):
+        tab = real(*args, **kw)
+        alive.append(weakref.ref(tab))
+        for o in others:
+            real(o, "others")
+        return tab
+
+    def launched(*args):
+        gc.collect()
+        assert alive[0]() is not None and alive[0]().data_ptr() in args
+
+    monkeypatch.setattr(plan, "ptr_table", made)
+    gpu.during[name] = launched
+    {"fs_pack": lambda: fs.fs_pack(plan, params, whole), "fs_unpack": lambda: fs.fs_unpack(plan, whole, params),
+     "fs_pack_cast": lambda: fs.fs_pack_cast(plan, params, whole), "fs_pack_mx4": lambda: fs.fs_pack_mx4(mp, params, whole4),
+     "fs_unpack_mx4": lambda: fs.fs_unpack_mx4(mp, whole4, params)}[name]()
+    assert gpu.calls[-1][0] == name
