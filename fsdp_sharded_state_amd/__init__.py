@@ -451,9 +451,10 @@ class Plan:
             tab = torch.tensor(ptrs or [0], dtype=torch.int64, device=dev)
             tab = _Table(tab, torch._C._cuda_getCurrentRawStream(tab.get_device()))
             if len(self._ptr_cache) >= 8:          # keep a few pointer sets (pack and unpack sides)
-                old = next((k for k in self._ptr_cache if k not in self._pinned), None)
+                # (a copy of the keys, and no error without the oldest: another thread may be at the same place)
+                old = next((k for k in list(self._ptr_cache) if k not in self._pinned), None)
                 if old is not None:
-                    self._ptr_cache.pop(old)
+                    self._ptr_cache.pop(old, None)
             self._ptr_cache[key] = tab
         handle = torch._C._cuda_getCurrentRawStream(tab.memory.get_device()) if stream is None else _stream(stream)
         bare = stream is not None and not isinstance(stream, torch.cuda.Stream)

@@ -53,3 +53,24 @@ def test_a_call_holds_its_table_until_it_has_launched(gpu, monkeypatch, name):
      "fs_pack_cast": lambda: fs.fs_pack_cast(plan, params, whole), "fs_pack_mx4": lambda: fs.fs_pack_mx4(mp, params, whole4),
      "fs_unpack_mx4": lambda: fs.fs_unpack_mx4(mp, whole4, params)}[name]()
     assert gpu.calls[-1][0] == name
+
+
+@pytest.mark.parametrize("change", ["releases", "adds"])
+def test_two_threads_may_release_sets_of_one_plan(gpu, change):
+    """Between one thread's look at the sets and its release of one, another may release the same or add its own."""
+    plan = fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2").upload()
+    sets = [[gpu.empty(8, 64)] for _ in range(9)]
+    for s in sets[:8]:
+        plan.ptr_table(s, "params")
+
+    class Pinned(set):
+        def __contains__(self, key):        # the other thread's turn
+            if change == "releases":
+                plan._ptr_cache.pop(key, None)
+                return False
+            if len(plan._ptr_cache) < 12:
+                plan._ptr_cache[len(plan._ptr_cache)] = None
+            return key == next(iter(plan._ptr_cache))
+
+    plan._pinned = Pinned()
+    assert plan.ptr_table(sets[8], "params").tolist() == [sets[8][0].data_ptr()]
