@@ -460,6 +460,7 @@ class Plan:
         bare = stream is not None and not isinstance(stream, torch.cuda.Stream)
         if not tab.read_on(stream, handle) or capturing or bare:
             self._pinned.add(key)
+            self._ptr_cache[key] = tab          # another thread may have released it before the pin was there
         return tab.memory
 
 

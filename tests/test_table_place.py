@@ -74,3 +74,22 @@ def test_two_threads_may_release_sets_of_one_plan(gpu, change):
 
     plan._pinned = Pinned()
     assert plan.ptr_table(sets[8], "params").tolist() == [sets[8][0].data_ptr()]
+
+
+def test_a_pinned_set_stays(gpu):
+    """Also where another thread released it between its lookup and its being pinned."""
+    plan = fs.fs_plan([(8, 64)], "bf16", 2, False, "fsdp2").upload()
+    params = [gpu.empty(8, 64)]
+    plan.ptr_table(params, "params")
+
+    class Pinned(set):
+        def add(self, key):
+            plan._ptr_cache.pop(key)        # the other thread's turn, before the pin is there
+            super().add(key)
+
+    plan._pinned = Pinned()
+    gpu.capturing = True
+    tab = plan.ptr_table(params, "params")
+    gpu.capturing = False
+    (key, held), = plan._ptr_cache.items()
+    assert held.memory is tab and key in plan._pinned
