@@ -248,6 +248,18 @@ def _read_on(table: Optional[_Table], stream) -> Optional[int]:
     return handle
 
 
+def _put(plan, fn, nbytes: int, device, stream):
+    """A plan's tables on a GPU, unless they are there already."""
+    where = torch.device(device)
+    if plan.workspace is not None and where.type == "cuda" and plan.workspace.get_device() == (
+            torch.cuda.current_device() if where.index is None else where.index):
+        return
+    table = _upload(fn, plan._h, nbytes, where, stream)
+    if plan._table is not None:
+        plan._earlier.append(plan._table)
+    plan._table, plan.workspace = table, table.memory
+
+
 def _upload(fn, plan, nbytes: int, device, stream) -> _Table:
     """The tables of a plan on a GPU, in memory of the stream that copies them:
     what another stream has under way could still write to memory of its own.
@@ -292,6 +304,7 @@ class Plan:
         self.info = info
         self.workspace: Optional[torch.Tensor] = None
         self._table: Optional[_Table] = None    # the workspace and who reads it
+        self._earlier: list = []                # those on other GPUs, which launches and captured graphs may still read
         self._ptr_cache = {}
         self._pinned = set()        # pointer-table keys a captured graph or another stream may still read
         self._pieces = {}           # rank -> local piece element counts
@@ -401,9 +414,9 @@ class Plan:
                                    _dev_ptr(shard, "shard") if shard.numel() else 0, _read_on(self._table, stream)))
 
     def upload(self, device="cuda", stream=None) -> "Plan":
-        """Put the tables on a GPU, copied on `stream`, and wait for them."""
-        self._table = _upload(lib().fs_plan_upload, self._h, self.info.workspace_bytes, device, stream)
-        self.workspace = self._table.memory
+        """Put the tables on a GPU, copied on `stream`, and wait for them.  They do not change, so where they are
+        there already they stay."""
+        _put(self, lib().fs_plan_upload, self.info.workspace_bytes, device, stream)
         return self
 
     def ptr_table(self, tensors: Sequence[torch.Tensor], what: str, elem_bytes: Optional[int] = None,
@@ -493,6 +506,7 @@ class Reshard:
         self.workspace_bytes, self.n_segments = wb.value, ns.value
         self.workspace: Optional[torch.Tensor] = None
         self._table: Optional[_Table] = None    # the workspace and who reads it
+        self._earlier: list = []                # those on other GPUs, which launches and captured graphs may still read
 
     def close(self):
         h = self.__dict__.pop("_h", None)
@@ -503,9 +517,8 @@ class Reshard:
         self.close()
 
     def upload(self, device="cuda", stream=None) -> "Reshard":
-        """Put the tables on a GPU, copied on `stream`, and wait for them."""
-        self._table = _upload(lib().fs_reshard_upload, self._h, self.workspace_bytes, device, stream)
-        self.workspace = self._table.memory
+        """As Plan.upload."""
+        _put(self, lib().fs_reshard_upload, self.workspace_bytes, device, stream)
         return self
 
 
@@ -1010,7 +1023,7 @@ class Mx4Plan:
         self.gathered_bytes, self.workspace_bytes = info.gathered_bytes, info.workspace_bytes
         self.workspace: Optional[torch.Tensor] = None
         self._table: Optional[_Table] = None    # the workspace and who reads it
-        self._earlier: list = []    # of earlier uploads, which launches and captured graphs may still read
+        self._earlier: list = []                # those on other GPUs, which launches and captured graphs may still read
 
     def close(self):
         h = self.__dict__.pop("_h", None)
@@ -1021,17 +1034,11 @@ class Mx4Plan:
         self.close()
 
     def upload(self, device="cuda", stream=None) -> "Mx4Plan":
-        """Put the tables on a GPU.  They do not change, so where they are there already they stay."""
+        """As Plan.upload."""
         where = torch.device(device)
         if where.type != "cuda":
             raise ValueError(f"fs_mx4_plan: the tables go to a GPU, not to {where}")
-        index = torch.cuda.current_device() if where.index is None else where.index
-        if self.workspace is not None and self.workspace.get_device() == index:
-            return self
-        table = _upload(lib().fs_mx4_plan_upload, self._h, self.workspace_bytes, torch.device("cuda", index), stream)
-        if self._table is not None:
-            self._earlier.append(self._table)
-        self._table, self.workspace = table, table.memory
+        _put(self, lib().fs_mx4_plan_upload, self.workspace_bytes, where, stream)
         return self
 
     def piece(self, i: int, rank: int) -> tuple:

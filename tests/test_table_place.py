@@ -93,3 +93,14 @@ def test_a_pinned_set_stays(gpu):
     gpu.capturing = False
     (key, held), = plan._ptr_cache.items()
     assert held.memory is tab and key in plan._pinned
+
+
+@pytest.mark.parametrize("kind", ["plan", "mx4", "reshard"])
+def test_tables_stay_where_they_are(gpu, kind):
+    """They do not change; a captured graph reads them at every replay, and a second upload may come in between."""
+    plans = [fs.fs_plan([(8, 64)], "bf16", n, False, "fsdp2") for n in (2, 4)]
+    p = {"plan": lambda: plans[0], "mx4": lambda: fs.fs_mx4_plan(plans[0]), "reshard": lambda: fs.fs_reshard_plan(*plans)}[kind]()
+    ws = weakref.ref(p.upload().workspace)
+    assert p.upload() is p and p.upload("cuda:0") is p
+    gc.collect()
+    assert ws() is p.workspace and len(gpu.calls) == 1
