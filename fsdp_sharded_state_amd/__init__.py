@@ -767,7 +767,7 @@ def _scalar_ptr(t: Optional[torch.Tensor], dtype: torch.dtype, index: Optional[i
         raise ValueError(f"{what} must be one {dtype} value")
     if t.get_device() != index:
         if index is not None and index >= 0:
-            raise ValueError(f"{what} is on {t.device}, the gradients on cuda:{index}")
+            raise ValueError(f"{what} is on {t.device}, the other arguments on cuda:{index}")
         if not t.is_cuda:
             raise ValueError(f"{what} must be a GPU tensor")
     return t.data_ptr()
