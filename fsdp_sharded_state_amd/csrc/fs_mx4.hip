@@ -601,7 +601,7 @@ int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, M
     const int64_t run = m->chunk_rows ? imin(m->chunk_rows, m->rows) : m->rows;   // rows of a chunk
     if ((run > 1 && (m->code_stride < nb * kMx4BlockBytes || m->scale_stride < nb)))
         return fail(FS_E_INVAL, "%s: the rows of %s overlap", what, name);
-    const int64_t chunks = m->chunk_rows ? (m->rows + m->chunk_rows - 1) / m->chunk_rows : 1;
+    const int64_t chunks = m->chunk_rows ? (m->rows - 1) / m->chunk_rows + 1 : 1;   // chunk_rows may be any length
     if (misaligned(m->codes, 16) || (run > 1 && (m->code_stride & 15)) || (chunks > 1 && (m->chunk_stride & 15)))
         return fail(FS_E_ALIGN, "%s: the codes of %s are not on 16 bytes", what, name);
     if ((run > 1 && (m->code_stride > kMost / run || m->scale_stride > kMost / run)) ||
