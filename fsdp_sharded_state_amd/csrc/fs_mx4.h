@@ -366,9 +366,25 @@ struct Mx4Mat {
 
 inline int64_t mx4_blocks(int64_t n) { return n / kMx4Block + (n % kMx4Block != 0); }
 
-// Checks a matrix argument (`m` not NULL) and gives its kernel form and the
-// bytes that its codes and scales span.
-int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, int64_t *code_span,
-                 int64_t *scale_span);
+// Memory that a call reads or writes: runs of `width` bytes, `stride` apart (0: one run), `span` bytes from the first
+// one's start to the last one's end.  A chunked matrix counts as one run, its gaps included.
+struct Footprint {
+    const void *p;
+    int64_t span, stride, width;
+    const char *name;
+};
+// Whether two meet.  Rows of one stride may lie between each other's, as a row's codes and scales side by side, and a
+// single run between rows; rows of two strides whose spans meet are taken to meet.
+inline bool meet(const Footprint &a, const Footprint &b) {
+    if (!ranges_overlap(a.p, a.span, b.p, b.span)) return false;
+    const int64_t s = a.stride ? a.stride : b.stride;
+    if (s == 0 || (b.stride && b.stride != s)) return true;
+    const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) % s, d = off < 0 ? off + s : off;
+    return d < a.width || b.width > s - d;   // a's rows reach into the next of b's, or b's into the next of a's
+}
+
+// Checks a matrix argument (`m` not NULL) and gives its kernel form and what
+// its codes and its scales cover.
+int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, Footprint (&covers)[2]);
 
 }  // namespace fsi

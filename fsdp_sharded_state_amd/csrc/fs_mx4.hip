@@ -586,10 +586,9 @@ extern "C" int fs_reduce_shard_mx4(fs_mx4_plan_t p, int32_t rank, int32_t grad_a
 
 namespace fsi {
 
-int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, int64_t *code_span,
-                 int64_t *scale_span) {
+int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, Mx4Mat *out, Footprint (&covers)[2]) {
     constexpr int64_t kMost = (int64_t)1 << 56;   // sums of these stay within int64
-    *code_span = *scale_span = 0;
+    covers[0] = covers[1] = Footprint{nullptr, 0, 0, 0, name};
     memset(out, 0, sizeof *out);
     if (m->rows < 0 || m->cols < 0) return fail(FS_E_INVAL, "%s: %s has a negative size", what, name);
     if (m->rows > INT32_MAX || m->cols > INT32_MAX)
@@ -613,12 +612,12 @@ int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, M
     if (chunks > 1 && (m->chunk_stride < codes || m->chunk_stride < scales))
         return fail(FS_E_INVAL, "%s: the chunks of %s overlap", what, name);
     const int64_t far = chunks > 1 ? (chunks - 1) * m->chunk_stride : 0;
-    *code_span = far + codes;
-    *scale_span = far + scales;
     out->codes = static_cast<const uint8_t *>(m->codes);
     out->scales = static_cast<const uint8_t *>(m->scales);
     out->code_stride = run > 1 ? m->code_stride : 0;
     out->scale_stride = run > 1 ? m->scale_stride : 0;
+    covers[0] = {m->codes, far + codes, chunks > 1 ? 0 : out->code_stride, chunks > 1 ? far + codes : nb * kMx4BlockBytes, name};
+    covers[1] = {m->scales, far + scales, chunks > 1 ? 0 : out->scale_stride, chunks > 1 ? far + scales : nb, name};
     if (chunks > 1) {
         uint32_t l = 0;
         while (((int64_t)1 << l) < m->chunk_rows) ++l;   // chunk_rows < rows < 2^31
@@ -634,36 +633,28 @@ int check_matrix(const char *what, const char *name, const fs_mx4_matrix_t *m, M
 
 namespace {
 
-struct Span {
-    const void *p;
-    int64_t bytes;
-    const char *name;
-};
-
-// Output matrix `m` of `rows` by `cols`; its codes and scales are appended to the spans, which must be disjoint of them.
+// Output matrix `m` of `rows` by `cols`; its codes and scales are appended to `all`, which must be disjoint of them.
 int check_out(const char *what, const char *name, const fs_mx4_matrix_t *m, int64_t rows, int64_t cols, Mx4Out *out,
-              Span *spans, int *count) {
+              Footprint *all, int *count) {
     Mx4Mat k;
-    int64_t code_span, scale_span;
+    Footprint mine[2];
     if (m->rows != rows || m->cols != cols)
         return fail(FS_E_INVAL, "%s: %s must be %lld by %lld", what, name, (long long)rows, (long long)cols);
     if (m->chunk_rows != 0) return fail(FS_E_INVAL, "%s: %s is chunked", what, name);
-    if (int rc = check_matrix(what, name, m, &k, &code_span, &scale_span)) return rc;
-    const Span mine[] = {{k.codes, code_span, name}, {k.scales, scale_span, name}};
-    for (const Span &s : mine) {
+    if (int rc = check_matrix(what, name, m, &k, mine)) return rc;
+    for (const Footprint &f : mine) {
         for (int i = 0; i < *count; ++i)
-            if (ranges_overlap(s.p, s.bytes, spans[i].p, spans[i].bytes))
-                return fail(FS_E_INVAL, "%s: %s overlaps %s", what, name, spans[i].name);
-        spans[(*count)++] = s;
+            if (meet(f, all[i])) return fail(FS_E_INVAL, "%s: %s overlaps %s", what, name, all[i].name);
+        all[(*count)++] = f;
     }
     *out = Mx4Out{const_cast<uint8_t *>(k.codes), const_cast<uint8_t *>(k.scales), k.code_stride, k.scale_stride};
     return FS_OK;
 }
 
-// Checks a plain matrix of `width` bytes an element and gives the bytes it spans.
+// Checks a plain matrix of `width` bytes an element and gives what it covers.
 int check_plain(const char *what, const char *name, const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t width,
-                int64_t *span) {
-    *span = 0;
+                Footprint *covers) {
+    *covers = Footprint{nullptr, 0, 0, 0, name};
     if (rows < 0 || cols < 0) return fail(FS_E_INVAL, "%s: negative size", what);
     if (rows > INT32_MAX || cols > INT32_MAX) return fail(FS_E_OVERFLOW, "%s: more than 2^31 - 1 rows or columns", what);
     if (rows == 0 || cols == 0) return FS_OK;
@@ -671,7 +662,8 @@ int check_plain(const char *what, const char *name, const void *p, int64_t rows,
     if (misaligned(p, width)) return fail(FS_E_ALIGN, "%s: %s not aligned to its element size", what, name);
     if (rows > 1 && ld < cols) return fail(FS_E_INVAL, "%s: the rows of %s overlap", what, name);
     if (rows > 1 && ld > ((int64_t)1 << 56) / rows) return fail(FS_E_OVERFLOW, "%s: %s is too large", what, name);
-    *span = ((rows > 1 ? (rows - 1) * ld : 0) + cols) * width;
+    const int64_t stride = rows > 1 ? ld * width : 0;
+    *covers = Footprint{p, (rows - 1) * stride + cols * width, stride, cols * width, name};
     return FS_OK;
 }
 
@@ -693,17 +685,15 @@ extern "C" int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dty
     if (int rc = check_dtype(what, dtype)) return rc;
     if (!by_row && !by_col) return fail(FS_E_INVAL, "%s: no output", what);
     if (int rc = check_seed(what, seed)) return rc;
-    Span spans[6];
+    Footprint all[6];
     int count = 0;
-    int64_t span;
-    if (int rc = check_plain(what, "x", x, rows, cols, ldx, width(dtype), &span)) return rc;
-    spans[count++] = Span{x, span, "x"};
-    spans[count++] = Span{seed, seed ? 8 : 0, "seed"};
+    if (int rc = check_plain(what, "x", x, rows, cols, ldx, width(dtype), &all[count++])) return rc;
+    all[count++] = Footprint{seed, seed ? 8 : 0, 0, 8, "seed"};
     Mx4Out row{}, col{};
     if (by_row)
-        if (int rc = check_out(what, "by_row", by_row, rows, cols, &row, spans, &count)) return rc;
+        if (int rc = check_out(what, "by_row", by_row, rows, cols, &row, all, &count)) return rc;
     if (by_col)
-        if (int rc = check_out(what, "by_col", by_col, cols, rows, &col, spans, &count)) return rc;
+        if (int rc = check_out(what, "by_col", by_col, cols, rows, &col, all, &count)) return rc;
     uint32_t across, tiles;
     if (int rc = by_col ? mat_tiles(what, rows, cols, kColTileRows, dtype == FS_BF16 ? kColTileCols<uint16_t> : kColTileCols<float>, &across, &tiles)
                         : mat_tiles(what, rows, cols, kRowTileRows, kRowTileCols, &across, &tiles))
@@ -739,11 +729,10 @@ extern "C" int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype d
     if (!m) return fail(FS_E_INVAL, "%s: the matrix is NULL", what);
     if (int rc = check_dtype(what, dtype)) return rc;
     Mx4Mat k;
-    int64_t code_span, scale_span, span;
-    if (int rc = check_matrix(what, "the matrix", m, &k, &code_span, &scale_span)) return rc;
-    if (int rc = check_plain(what, "out", out, m->rows, m->cols, ldo, width(dtype), &span)) return rc;
-    if (ranges_overlap(out, span, k.codes, code_span) || ranges_overlap(out, span, k.scales, scale_span))
-        return fail(FS_E_INVAL, "%s: out overlaps the matrix", what);
+    Footprint read[2], written;
+    if (int rc = check_matrix(what, "the matrix", m, &k, read)) return rc;
+    if (int rc = check_plain(what, "out", out, m->rows, m->cols, ldo, width(dtype), &written)) return rc;
+    if (meet(written, read[0]) || meet(written, read[1])) return fail(FS_E_INVAL, "%s: out overlaps the matrix", what);
     uint32_t across, tiles;
     if (int rc = mat_tiles(what, m->rows, m->cols, kRowTileRows, kRowTileCols, &across, &tiles)) return rc;
     if (tiles == 0) return FS_OK;

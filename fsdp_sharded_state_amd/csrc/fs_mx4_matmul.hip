@@ -569,9 +569,9 @@ extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b,
     if (!a || !b) return fail(FS_E_INVAL, "%s: a matrix is NULL", what);
     if (dtype != FS_BF16 && dtype != FS_FP32) return fail(FS_E_DTYPE, "%s: unknown dtype %d", what, (int)dtype);
     Mx4Mat ka, kb;
-    int64_t ac, as, bc, bs;
-    if (int rc = check_matrix(what, "a", a, &ka, &ac, &as)) return rc;
-    if (int rc = check_matrix(what, "b", b, &kb, &bc, &bs)) return rc;
+    Footprint ra[2], rb[2];
+    if (int rc = check_matrix(what, "a", a, &ka, ra)) return rc;
+    if (int rc = check_matrix(what, "b", b, &kb, rb)) return rc;
     if (a->cols != b->cols)
         return fail(FS_E_INVAL, "%s: a has %lld columns, b %lld", what, (long long)a->cols, (long long)b->cols);
     const int64_t m = a->rows, n = b->rows, k = a->cols, w = dtype == FS_BF16 ? 2 : 4;
@@ -580,11 +580,10 @@ extern "C" int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b,
     if (misaligned(out, w)) return fail(FS_E_ALIGN, "%s: out not aligned to its element size", what);
     if (m > 1 && ldo < n) return fail(FS_E_INVAL, "%s: the rows of out overlap", what);
     if (m > 1 && ldo > ((int64_t)1 << 56) / m) return fail(FS_E_OVERFLOW, "%s: out is too large", what);
-    const int64_t span = ((m > 1 ? (m - 1) * ldo : 0) + n) * w;
-    struct { const void *p; int64_t bytes; } in[] = {{ka.codes, ac}, {ka.scales, as}, {kb.codes, bc}, {kb.scales, bs}};
-    for (const auto &s : in)
-        if (ranges_overlap(out, span, s.p, s.bytes)) return fail(FS_E_INVAL, "%s: out overlaps a matrix", what);
     const int64_t nb = mx4_blocks(k), ld = m > 1 ? ldo : 0;
+    const Footprint written{out, ((m - 1) * ld + n) * w, ld * w, n * w, "out"};
+    for (const Footprint &f : {ra[0], ra[1], rb[0], rb[1]})
+        if (meet(written, f)) return fail(FS_E_INVAL, "%s: out overlaps a matrix", what);
     (void)hipGetLastError();
     // By the tiles that there are for 256 CUs, measured over m from 1 to 4096, n and k from 512 to 11008 (us, in a graph).
     // 16 by 16 up to 512 tiles, or where 16 rows are all: 4.4 for 5.9 of the next (1 by 4096 by 4096), 7.1 for 8.9 (1 by

@@ -610,7 +610,11 @@ int fs_adamw_step_clip(int64_t n, float *master, float *exp_avg, float *exp_avg_
  * its scales at scales + r * scale_stride.  With chunk_rows > 0 the rows lie
  * in chunks of that many, chunk_stride bytes apart (in codes and in scales
  * alike), and the strides count within a chunk.  codes, code_stride and
- * chunk_stride are multiples of 16. */
+ * chunk_stride are multiples of 16.
+ *
+ * Rows of one stride, in bytes, may lie between each other's: a row's scales after its
+ * codes, a call's output beside its input.  What overlaps otherwise is judged
+ * by the whole span from the first row's start to the last one's end, and so is a chunked matrix. */
 typedef struct {
     void *codes;
     void *scales;

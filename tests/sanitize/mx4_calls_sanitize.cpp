@@ -86,6 +86,30 @@ static fs_mx4_matrix_t matrix(int64_t rows, int64_t cols) {
     return m;
 }
 
+// Rows of codes and of scales side by side in one buffer share no byte, and are not refused; rows that do, are.
+static void rows_between_rows() {
+    char *buf = reinterpret_cast<char *>(1ll << 30);
+    for (int64_t stride = 48; stride <= 80; stride += 16)
+        for (int64_t at = 0; at < stride; ++at) {
+            fs_mx4_matrix_t m = {buf, buf + at, 5, 70, stride, stride, 0, 0};      // 48 bytes of codes, 3 of scales
+            const int rc = fs_mx4_quantize(5, 70, reinterpret_cast<void *>(1 << 20), FS_FP32, 70, &m, nullptr, nullptr, nullptr);
+            EXPECT(rc == (at >= 48 && at + 3 <= stride ? FS_OK : FS_E_INVAL), "stride %lld, scales at %lld: %d %s", (long long)stride, (long long)at, rc, fs_last_error());
+        }
+    // the plain matrix and its codes in one buffer, and a product's output beside its operand's rows
+    fs_mx4_matrix_t m = {buf + 288, reinterpret_cast<void *>(1ll << 35), 5, 70, 336, 3, 0, 0};
+    EXPECT(fs_mx4_quantize(5, 70, buf, FS_FP32, 84, &m, nullptr, nullptr, nullptr) == FS_OK, "%s", fs_last_error());
+    EXPECT(fs_mx4_dequantize(&m, buf, FS_FP32, 84, nullptr) == FS_OK, "%s", fs_last_error());
+    EXPECT(fs_mx4_dequantize(&m, buf + 12, FS_FP32, 84, nullptr) == FS_E_INVAL, "out reaches into the codes");
+    EXPECT(fs_mx4_dequantize(&m, buf + 56, FS_FP32, 84, nullptr) == FS_E_INVAL, "the codes reach into out");
+    EXPECT(fs_mx4_dequantize(&m, buf, FS_FP32, 85, nullptr) == FS_E_INVAL, "another stride");
+    fs_mx4_matrix_t b = {reinterpret_cast<void *>(1ll << 36), reinterpret_cast<void *>(1ll << 37), 72, 70, 48, 3, 0, 0};
+    EXPECT(fs_mx4_matmul(&m, &b, buf, FS_FP32, 84, nullptr) == FS_OK, "%s", fs_last_error());
+    EXPECT(fs_mx4_matmul(&m, &b, buf + 4, FS_FP32, 84, nullptr) == FS_E_INVAL, "out reaches into the codes");
+    // a seed between rows
+    EXPECT(fs_mx4_quantize(5, 70, buf, FS_FP32, 84, &m, nullptr, reinterpret_cast<const uint64_t *>(buf + 280), nullptr) == FS_OK, "%s", fs_last_error());
+    EXPECT(fs_mx4_quantize(5, 70, buf, FS_FP32, 84, &m, nullptr, reinterpret_cast<const uint64_t *>(buf + 336 + 328), nullptr) == FS_E_INVAL, "a seed in the codes");
+}
+
 int main() {
     long done = 0;
     for (int i = 0; i < 400000; ++i) {
@@ -116,6 +140,7 @@ int main() {
         fs_mx4_matrix_t m = {reinterpret_cast<void *>(1 << 20), reinterpret_cast<void *>(1 << 24), 40, 70, 48, 3, n, 0};
         EXPECT(fs_mx4_dequantize(&m, reinterpret_cast<void *>(1ll << 30), FS_FP32, 70, nullptr) == FS_OK, "chunks of %lld rows: %s", (long long)n, fs_last_error());
     }
+    rows_between_rows();
     EXPECT(done > 1000, "only %ld calls came to a launch", done);
     if (g_fail) return 1;
     printf("ok: %ld calls came to a launch\n", done);
