@@ -220,30 +220,32 @@ class _Table:
     was taken on; every other stream that reads it is recorded, once, so that
     the allocator waits for that one too."""
 
+    __slots__ = ("memory", "index", "known")
+
     def __init__(self, memory: torch.Tensor, handle: int):
-        self.memory = memory
-        self._known = {handle} - {_PER_THREAD_STREAM}
+        self.memory, self.index = memory, memory.get_device()
+        self.known = {handle} - {_PER_THREAD_STREAM}    # handles of the streams that need no more
 
     def read_on(self, stream, handle: int) -> bool:
         """A launch on `stream` (None: the current one), whose handle this is,
         reads the memory.  False where the allocator cannot be told: a bare
         handle may be destroyed before the memory is given back, and the
         per-thread default stream is another one in every thread."""
-        if handle in self._known:
+        if handle in self.known:
             return True
         if stream is None:
             stream = torch.cuda.current_stream(self.memory.device)
         if handle == _PER_THREAD_STREAM or not isinstance(stream, torch.cuda.Stream):
             return False
         self.memory.record_stream(stream)
-        self._known.add(handle)
+        self.known.add(handle)
         return True
 
 
 def _read_on(table: Optional[_Table], stream) -> Optional[int]:
     """The handle of the stream of a launch that reads a plan's tables (None: it has none yet, which the call refuses)."""
     handle = _stream(stream)
-    if table is not None:
+    if table is not None and handle not in table.known:
         table.read_on(stream, handle)
     return handle
 
@@ -469,7 +471,9 @@ class Plan:
                 if old is not None:
                     self._ptr_cache.pop(old, None)
             self._ptr_cache[key] = tab
-        handle = torch._C._cuda_getCurrentRawStream(tab.memory.get_device()) if stream is None else _stream(stream)
+        handle = torch._C._cuda_getCurrentRawStream(tab.index) if stream is None else _stream(stream)
+        if stream is None and not capturing and handle in tab.known:
+            return tab.memory
         bare = stream is not None and not isinstance(stream, torch.cuda.Stream)
         if not tab.read_on(stream, handle) or capturing or bare:
             self._pinned.add(key)
@@ -792,7 +796,7 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1, table: Optional[_T
         handle = _stream(stream)
         if isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
             raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
-    if table is not None:
+    if table is not None and handle not in table.known:
         table.read_on(stream, handle)
     if scratch < 0:
         return _check(fn(*args, handle))

@@ -45,11 +45,11 @@ def test_a_plan_on_another_stream_than_its_upload(kind):
         torch.cuda.synchronize()
     assert torch.equal(here[0], there[0]) and torch.equal(here[2], there[2]) and all(map(torch.equal, here[1], there[1]))
     if kind != "handle":
-        assert s.cuda_stream in mp._table._known
+        assert s.cuda_stream in mp._table.known
         # the parameters' table and that of the outputs there; the outputs here have one of their own
-        assert sum(s.cuda_stream in t._known for t in plan._ptr_cache.values()) == 2 and not plan._pinned
+        assert sum(s.cuda_stream in t.known for t in plan._ptr_cache.values()) == 2 and not plan._pinned
     else:
-        assert s.cuda_stream not in mp._table._known and len(plan._pinned) == len(plan._ptr_cache) == 3
+        assert s.cuda_stream not in mp._table.known and len(plan._pinned) == len(plan._ptr_cache) == 3
 
 
 def test_tables_uploaded_and_read_on_a_side_stream():
