@@ -1,4 +1,6 @@
 """The 4-bit calls' plans on several streams, and uploads between captures."""
+import threading
+
 import pytest
 import torch
 
@@ -108,3 +110,76 @@ def test_a_captured_graph_reads_the_tables_it_was_captured_with():
         step(sets[0])                       # eager, from the last upload's tables
         torch.cuda.synchronize()
         assert all(map(torch.equal, state(sets[0]), want[0]))
+
+
+def test_a_captured_dequantisation_replays_with_new_values():
+    """Of a matrix and of a gathered weight in chunks, into bf16 and fp32."""
+    params, plan, mp = _group(4)
+    gathered = torch.empty(mp.gathered_bytes, dtype=torch.uint8, device="cuda")
+    fs.fs_pack_mx4(mp, params, gathered)
+    q, w = fs.fs_mx4_empty(77, 130), mp.matrix(gathered, 1)
+    x = torch.randn(77, 130, generator=torch.Generator(device="cuda").manual_seed(5), device="cuda")
+    fs.fs_mx4_quantize(x, q)
+    outs = [torch.empty(s, dtype=t, device="cuda") for t in (torch.bfloat16, torch.float32) for s in (q.shape, w.shape)]
+
+    def step():
+        for k, o in enumerate(outs):
+            fs.fs_mx4_dequantize(w if k % 2 else q, o)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(4):
+        fs.fs_mx4_quantize(x * (turn + 2), q)
+        fs.fs_pack_mx4(mp, [p * (turn + 2) for p in params], gathered)
+        for o in outs:
+            o.zero_()
+        say("replay", turn)
+        graph.replay()
+        got = [o.clone() for o in outs]
+        torch.cuda.synchronize()
+        step()
+        assert all(map(torch.equal, got, outs)) and all((o != 0).any() for o in outs), f"turn {turn}"
+
+
+def test_threads_on_one_plan():
+    """Each on a stream of its own and with more sets of parameters than the plan keeps tables of, some shared with the
+    other threads: every result is the single-threaded one."""
+    _, plan, mp = _group(6)
+    sets = [[torch.randn(s, generator=torch.Generator(device="cuda").manual_seed(10 * k + i), device="cuda").bfloat16()
+             for i, s in enumerate(SHAPES)] for k in range(14)]
+    want = []
+    for params in sets:
+        b = _buffers(mp, params)
+        fs.fs_pack_mx4(mp, params, b[0])
+        fs.fs_unpack_mx4(mp, b[0], b[1])
+        want.append((b[0], b[1]))
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for turn in range(6):
+                    got = []
+                    for j in [*range(3 * k, 3 * k + 3), 12, 13]:        # 12 and 13 are everyone's
+                        b = _buffers(mp, sets[j])
+                        fs.fs_pack_mx4(mp, sets[j], b[0], stream=stream if turn % 2 else None)
+                        fs.fs_unpack_mx4(mp, b[0], b[1], stream=stream if turn % 2 else None)
+                        got.append((j, b))
+                    stream.synchronize()
+                    for j, b in got:
+                        assert torch.equal(b[0], want[j][0]) and all(map(torch.equal, b[1], want[j][1])), f"thread {k}, turn {turn}, set {j}"
+        except Exception as e:     # noqa: BLE001
+            errors.append(e)
+
+    say("four threads on one plan")
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
