@@ -22,7 +22,8 @@ constexpr int kWavesExchanging = kUnits<T> > 1 ? kThreads / 64 : 1;
 
 // Copy-in: a tile a workgroup, all its loads on their way before the first block is made.  Its codes and scales
 // go through LDS: 16 bytes a lane are stored for the four that a lane makes at a time, and four scales
-// for one.  HBM bounds it: one 7B block in bf16 78 us, 6.6 TB/s.
+// for one.  HBM bounds it: one 7B block in bf16 78 to 81 us, 6.3 to 6.6 TB/s, with its buffers again and again, 94 with
+// buffers in turn that are in no cache.  At random 97 and 98: there the vector instructions do.
 template <class T, bool STOCHASTIC>
 __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__restrict__ tiles, uint32_t ntiles,
                                                             const Mx4Run *__restrict__ pads,
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(kThreads) void pack_mx4_kernel(const Mx4Tile *__res
 }
 
 // Copy-out: a lane makes 16 bytes of values at a time, whole cache lines a wave.  HBM bounds it: one 7B block in bf16
-// 73 us, 7.0 TB/s.
+// 73 to 75 us, 6.8 to 7.0 TB/s, again and again or right after its copy-in; 99, 5.2 TB/s, with buffers in turn.
 template <class T>
 __global__ __launch_bounds__(kThreads) void unpack_mx4_kernel(const Mx4Tile *__restrict__ tiles,
                                                               const uint8_t *__restrict__ gathered,
@@ -276,7 +277,9 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_mx4_kernel(int64_t row
     }
 }
 
-// Back: a lane takes a unit of U rows of the tile.  HBM bounds it: 8192 by 11008 to bf16 37 us, 6.2 TB/s, to fp32 62, 6.6.
+// Back: a lane takes a unit of U rows of the tile.  8192 by 11008 to bf16 takes 31 to 37 us, 6.2 to 7.3 TB/s, where the codes
+// are in the caches still (right after their making, or the same buffers again and again), to fp32 57 to 62; with buffers
+// in turn that are in no cache 51 and 99, 4.5 and 4.1 TB/s, two thirds of a copy's rate.
 template <class T>
 __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int64_t rows, int64_t cols, T *__restrict__ out,
                                                                   int64_t ldo, uint32_t tiles_x) {
@@ -308,9 +311,11 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
 // Along columns, with or without rows: a workgroup takes 128 rows by 256 bytes, and the columns' blocks come from a
 // copy in LDS.  There a lane takes 32 rows of a word, one or two blocks of its own, so no
 // lanes join; the lanes of a quad take the column's four blocks, which they store side by side.
-// 8192 by 11008 bf16 both ways: 66 us to nearest, 4.2 TB/s, which HBM and the LDS copy bound; 93 random, bound by the vector
+// 8192 by 11008 bf16 both ways: 62 to 66 us to nearest, 4.2 to 4.5 TB/s, which HBM and the LDS copy bound; 86 to 94 random,
+// bound by the vector
 // instructions, of which the random bits' multiplications (28 for 16 elements) take several times an addition's cycles.
-// Columns alone 55 and 58.  From fp32 105 and 123, 4.3 and 3.7 TB/s.
+// Columns alone 51 to 55 and 53 to 58.  From fp32 99 to 105 and 119 to 123.  With buffers in turn that are in no cache 76 and 88,
+// columns alone 57 and 60, from fp32 117 and 122.
 constexpr int kColTileRows = 128;
 template <class T>
 constexpr int kColTileCols = 256 / sizeof(T);

@@ -16,8 +16,9 @@
  *
  * Conventions for every call:
  *   - Device buffers are owned by the caller.  The library allocates no
- *     device memory and never synchronizes the device, except fs_plan_upload
- *     and fs_reshard_upload (set-up calls that wait for their own copies).
+ *     device memory and never synchronizes the device, except fs_plan_upload,
+ *     fs_reshard_upload and fs_mx4_plan_upload (set-up calls that wait for
+ *     their own copies).
  *   - Pointers named "device" point to GPU memory; pointers named "host" to
  *     CPU memory.  Every device pointer must be aligned to its element size
  *     (2 bytes for bf16, 4 for fp32); 16-byte alignment is not required but
@@ -31,7 +32,8 @@
  *     reduce dtype, 64M for AdamW), which measured faster than one launch
  *     over the whole buffer.  The calls that give a norm end with one or two
  *     more that join the partial totals, and a list call launches one kernel
- *     per 192 tensors; small calls of both are a single launch.
+ *     per 192 tensors; small calls of both are a single launch.  The 4-bit
+ *     calls launch one kernel, their reduce one per 64 slices.
  *   - fs_plan_info, fs_plan_param, fs_plan_segments, fs_plan_upload,
  *     fs_plan_destroy, the fs_reshard_info/upload/destroy calls and
  *     fs_last_error are infrastructure around the method's steps (reading a
@@ -645,8 +647,9 @@ typedef struct {
  * between their rows.
  * Errors: FS_E_INVAL (negative sizes, NULL pointers, both outputs NULL, wrong
  * sizes or strides, a chunked output, outputs that overlap x, the seed or each
- * other), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW (too large for one launch),
- * FS_E_HIP.
+ * other), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW (too large for one launch:
+ * more than 2^24 - 1 tiles of 16 rows by 128 columns, or with by_col of 128
+ * rows by 256 bytes), FS_E_HIP.
  */
 int fs_mx4_quantize(int64_t rows, int64_t cols, const void *x, fs_dtype dtype, int64_t ldx,
                     const fs_mx4_matrix_t *by_row, const fs_mx4_matrix_t *by_col,
@@ -681,7 +684,8 @@ int fs_mx4_dequantize(const fs_mx4_matrix_t *m, void *out, fs_dtype dtype, int64
  * dW = dy^T x are three such products: of x and W by row, of dy by row and W
  * by column, of dy and x by column.
  * Errors: FS_E_INVAL (NULL pointers, different cols, strides too small, out
- * overlapping a matrix), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW, FS_E_HIP.
+ * overlapping a matrix), FS_E_DTYPE, FS_E_ALIGN, FS_E_OVERFLOW (also too many outputs
+ * for one launch: with at most 16 rows in a, more than 134 million in b), FS_E_HIP.
  */
 int fs_mx4_matmul(const fs_mx4_matrix_t *a, const fs_mx4_matrix_t *b, void *out, fs_dtype dtype,
                   int64_t ldo, hipStream_t stream);
@@ -721,6 +725,7 @@ void fs_mx4_plan_destroy(fs_mx4_plan_t p);
  * fs_mx4_plan_matrix -- parameter i of a gathered buffer as a matrix of d0
  * rows (host only; nothing is read), for fs_mx4_matmul and fs_mx4_dequantize.
  * Needs an FSDP2 plan, whose chunks are whole rows, and rows of whole blocks.
+ * A parameter whose rows have no elements is a matrix without rows.
  * Errors: FS_E_INVAL (NULL, i out of range), FS_E_ALIGN (gathered not 16-byte
  * aligned), FS_E_UNSUPPORTED (FSDP1, or rows that are not a multiple of 32).
  */
