@@ -33,6 +33,7 @@ import ctypes
 import math
 import operator
 import os
+import threading
 from typing import List, Optional, Sequence
 
 import torch
@@ -250,16 +251,21 @@ def _read_on(table: Optional[_Table], stream) -> Optional[int]:
     return handle
 
 
+_putting = threading.Lock()
+
+
 def _put(plan, fn, nbytes: int, device, stream):
-    """A plan's tables on a GPU, unless they are there already."""
+    """A plan's tables on a GPU, unless they are there already.  One thread at
+    a time, so that the library has the tables that the plan keeps."""
     where = torch.device(device)
-    if plan.workspace is not None and where.type == "cuda" and plan.workspace.get_device() == (
-            torch.cuda.current_device() if where.index is None else where.index):
-        return
-    table = _upload(fn, plan._h, nbytes, where, stream)
-    if plan._table is not None:
-        plan._earlier.append(plan._table)
-    plan._table, plan.workspace = table, table.memory
+    with _putting:
+        if plan.workspace is not None and where.type == "cuda" and plan.workspace.get_device() == (
+                torch.cuda.current_device() if where.index is None else where.index):
+            return
+        table = _upload(fn, plan._h, nbytes, where, stream)
+        if plan._table is not None:
+            plan._earlier.append(plan._table)
+        plan._table, plan.workspace = table, table.memory
 
 
 def _upload(fn, plan, nbytes: int, device, stream) -> _Table:

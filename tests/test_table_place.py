@@ -1,5 +1,6 @@
 """Where the tables of pointer sets lie, and how long.  Host side only (tests/fake_gpu.py)."""
 import gc
+import threading
 import weakref
 
 import pytest
@@ -104,3 +105,21 @@ def test_tables_stay_where_they_are(gpu, kind):
     assert p.upload() is p and p.upload("cuda:0") is p
     gc.collect()
     assert ws() is p.workspace and len(gpu.calls) == 1
+
+
+@pytest.mark.parametrize("kind", ["plan", "mx4", "reshard"])
+def test_two_threads_may_upload_one_plan(gpu, kind):
+    """The second one waits and finds the tables there; two copies at once could leave the library with the one that is dropped."""
+    plans = [fs.fs_plan([(8, 64)], "bf16", n, False, "fsdp2") for n in (2, 4)]
+    p = {"plan": lambda: plans[0], "mx4": lambda: fs.fs_mx4_plan(plans[0]), "reshard": lambda: fs.fs_reshard_plan(*plans)}[kind]()
+    other = threading.Thread(target=p.upload)
+
+    def copying(*args):
+        if not gpu.calls[1:]:
+            other.start()
+            other.join(0.3)
+
+    gpu.during[{"plan": "fs_plan_upload", "mx4": "fs_mx4_plan_upload", "reshard": "fs_reshard_upload"}[kind]] = copying
+    p.upload()
+    other.join()
+    assert len(gpu.calls) == 1 and p.workspace.data_ptr() == gpu.calls[0][1][1]
