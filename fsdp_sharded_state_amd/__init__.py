@@ -787,9 +787,8 @@ def _launch(index: int, stream, fn, *args, scratch: int = -1, table: Optional[_T
     """Run a launching call with GPU `index` current, on `stream` (default:
     that GPU's current stream).  table: what the call reads of a plan (None
     also where a plan has none yet, which the call refuses).  scratch >= 0:
-    that many workspace bytes and
-    their count go before the stream; they belong to the stream the kernels
-    run on, so the allocator hands them out again in that stream's order.  The
+    that many workspace bytes and their count go before the stream; they
+    belong to the stream the kernels run on, so the allocator hands them out again in that stream's order.  The
     per-thread default stream is refused there: it is a stream of its own in
     every host thread, but has one handle, so the allocator would hand one
     thread's workspace to another while it is in use."""

@@ -312,8 +312,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx4_kernel(Mx4Mat m, int6
 // copy in LDS.  There a lane takes 32 rows of a word, one or two blocks of its own, so no
 // lanes join; the lanes of a quad take the column's four blocks, which they store side by side.
 // 8192 by 11008 bf16 both ways: 62 to 66 us to nearest, 4.2 to 4.5 TB/s, which HBM and the LDS copy bound; 86 to 94 random,
-// bound by the vector
-// instructions, of which the random bits' multiplications (28 for 16 elements) take several times an addition's cycles.
+// bound by the vector instructions, of which the random bits' multiplications (28 for 16 elements) take several times an
+// addition's cycles.
 // Columns alone 51 to 55 and 53 to 58.  From fp32 99 to 105 and 119 to 123.  With buffers in turn that are in no cache 76 and 88,
 // columns alone 57 and 60, from fp32 117 and 122.
 constexpr int kColTileRows = 128;

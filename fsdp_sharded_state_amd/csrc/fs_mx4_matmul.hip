@@ -196,10 +196,9 @@ __global__ __launch_bounds__(S::kThreads) void matmul_mx4_small_kernel(Mx4Mat a,
 // the start of a tile nor the writing of its outputs leaves the loads idle.
 // Outputs go through LDS, a part of a wave's tile at a time, so that stores cover whole cache lines.
 //
-// 8192 by 11008 by 4096 to bf16 takes 196 to 206 us, 3.6 to 3.8 PFLOP/s, 11008 by 4096 by 8192 to fp32 187 to 200, 3.7 to 3.9,
-// from one MI355X to another.  The
-// matrix instructions alone, on data, run at 6.8 PFLOP/s here, as power holds the clock under 1.9 GHz: 109 us.  With the
-// rounds' waits and LDS reads and without loads they take 135 to 140, the loads add about 23, the scales 9 of them, and
+// 8192 by 11008 by 4096 to bf16 takes 194 to 206 us, 3.6 to 3.8 PFLOP/s, 11008 by 4096 by 8192 to fp32 187 to 200, 3.7 to 3.9,
+// from one MI355X to another.  The matrix instructions alone, on data, run at 6.8 PFLOP/s here, as power holds the clock
+// under 1.9 GHz: 109 us.  With the rounds' waits and LDS reads and without loads they take 135 to 140, the loads add about 23, the scales 9 of them, and
 // the outputs the rest; 1376 and 688 tiles are 5.4 of 6 turns of 256 workgroups and 2.7 of 3.
 
 constexpr int kStepBlocks = 4;       // blocks of k in a step
